@@ -265,6 +265,84 @@ nvfp4_status nvfp4_fp8_gemm(const uint8_t *a8, const float *a_s_dec, const uint8
                             const float *b_s_dec, int64_t M, int64_t N, int64_t K, void *y_bf16,
                             const nvfp4_fused_out *fused, nvfp4_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Around a projection: the norms before and after a block, and the low-rank
+ * adapters of the requests in a batch.  No counterpart on the pages; they are
+ * what a transformer block does directly before, beside and after its NVFP4
+ * projections.
+ * ---------------------------------------------------------------------- */
+
+typedef enum {
+    NVFP4_BF16 = 0,
+    NVFP4_F32 = 1
+} nvfp4_dtype;
+
+typedef enum {
+    NVFP4_NORM_NONE = 0,
+    NVFP4_NORM_RMS = 1,  /* v / sqrt(mean(v^2) + eps) * weight + bias */
+    NVFP4_NORM_LAYER = 2 /* (v - mean) / sqrt(mean((v - mean)^2) + eps) * weight + bias */
+} nvfp4_norm;
+
+/* Arguments of nvfp4_residual_norm.  Row r of request g = row_group[r]:
+ *   z   = post(y[r])
+ *   h   = residual_scale * residual[r] + branch_scale * gate[g] * z
+ *   out = pre(h) * (1 + scale[g]) + shift[g]
+ * in fp32 throughout; h and out are rounded once, when they are stored (pre
+ * reads the unrounded h).  NULL leaves a step out: no y (h = residual_scale *
+ * residual, and post, gate and h are not given), no gate, scale or shift, no
+ * weight or bias; outputs that are NULL are not written.  At least one of h,
+ * out and q is.
+ *   rows, cols       rows >= 0, 16 <= cols <= 32768 with cols % 16 == 0
+ *   *_stride         elements from row to row (or request to request): a
+ *                    multiple of 8, at least cols; for gate, scale and shift
+ *                    also 0 (one vector for all)
+ *   residual, h      device, [rows, cols] of stream_dtype (an nvfp4_dtype)
+ *   y, out           device, [rows, cols] bf16
+ *   post_norm, pre_norm  nvfp4_norm values; weights, biases, gate, scale and
+ *                    shift are of vector_dtype (an nvfp4_dtype)
+ *   row_group        device, rows int32, the request of each row, or NULL:
+ *                    then rows / groups consecutive rows each (rows must be
+ *                    a multiple of groups).  A row whose request is not in
+ *                    [0, groups) is padding: it is not read, and its h, out,
+ *                    q, block scales, s_dec and amax stay as they were.
+ *   q, sf, s_dec_rows, amax_rows  the per-row NVFP4 quantization of out, bit
+ *                    for bit as nvfp4_quantize_rowwise gives it for the bf16
+ *                    out (amax_rows may be NULL); out itself may be NULL
+ * h may be the residual or y, and out may be y or the residual, where type
+ * and stride are the same; otherwise outputs must not overlap inputs. */
+typedef struct {
+    int64_t rows, cols;
+    const void *residual;
+    int64_t residual_stride;
+    const void *y;
+    int64_t y_stride;
+    void *h;
+    int64_t h_stride;
+    void *out;
+    int64_t out_stride;
+    const void *post_weight, *post_bias;
+    const void *pre_weight, *pre_bias;
+    const void *gate;
+    int64_t gate_stride;
+    const void *scale;
+    int64_t scale_stride;
+    const void *shift;
+    int64_t shift_stride;
+    const int32_t *row_group;
+    int64_t groups;
+    uint8_t *q;
+    uint8_t *sf;
+    float *s_dec_rows;
+    float *amax_rows;
+    float residual_scale, branch_scale;
+    float post_eps, pre_eps;
+    int post_norm, pre_norm;
+    int stream_dtype, vector_dtype;
+} nvfp4_residual_norm_args;
+
+/* One launch; see nvfp4_residual_norm_args. */
+nvfp4_status nvfp4_residual_norm(const nvfp4_residual_norm_args *args, nvfp4_stream_t stream);
+
 /* Failure-detection self-test (no counterpart on the pages): launches one
  * warp that waits, through the same bounded mbarrier wait every kernel of
  * this library uses, on a barrier that is never completed.  After

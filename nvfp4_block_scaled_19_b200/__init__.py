@@ -14,9 +14,11 @@ missing or the device is not sm_100, calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
+from typing import NamedTuple
 
 import torch
 
@@ -47,6 +49,19 @@ class LinearWorkspace(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("xq", ctypes.c_void_p), ("xsf", ctypes.c_void_p),
                 ("amax", ctypes.c_void_p), ("s_dec", ctypes.c_void_p), ("y", ctypes.c_void_p),
                 ("dyn_ws", ctypes.c_void_p)]
+
+
+class ResidualNormArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("rows", "cols")] +
+                [f for n in ("residual", "y", "h", "out")
+                 for f in ((n, ctypes.c_void_p), (n + "_stride", ctypes.c_int64))] +
+                [(n, ctypes.c_void_p) for n in ("post_weight", "post_bias", "pre_weight", "pre_bias")] +
+                [f for n in ("gate", "scale", "shift")
+                 for f in ((n, ctypes.c_void_p), (n + "_stride", ctypes.c_int64))] +
+                [("row_group", ctypes.c_void_p), ("groups", ctypes.c_int64)] +
+                [(n, ctypes.c_void_p) for n in ("q", "sf", "s_dec_rows", "amax_rows")] +
+                [(n, ctypes.c_float) for n in ("residual_scale", "branch_scale", "post_eps", "pre_eps")] +
+                [(n, ctypes.c_int) for n in ("post_norm", "pre_norm", "stream_dtype", "vector_dtype")])
 
 
 _lib = None
@@ -92,6 +107,8 @@ def lib() -> ctypes.CDLL:
         L.nvfp4_fp8_quantize.argtypes = [vp, i64, i64, vp, vp, vp, vp]
         L.nvfp4_fp8_gemm.restype = st
         L.nvfp4_fp8_gemm.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, vp, vp]
+        L.nvfp4_residual_norm.restype = st
+        L.nvfp4_residual_norm.argtypes = [ctypes.POINTER(ResidualNormArgs), vp]
         L.nvfp4_selftest_wait_timeout.restype = st
         L.nvfp4_selftest_wait_timeout.argtypes = [i64, vp]
         L.nvfp4_linear_host.restype = st
@@ -399,6 +416,185 @@ class NVFP4Linear:
                 "amax": torch.empty(1, dtype=torch.float32, device=dev),
                 "s_dec": torch.empty(1, dtype=torch.float32, device=dev),
                 "y": torch.empty(M, self.N, dtype=torch.bfloat16, device=dev)}
+
+
+def _raw_stream(device, stream) -> int:
+    """The given stream, or the current stream of the tensors' device."""
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+@contextlib.contextmanager
+def _other_device(device):
+    with torch.cuda.device(device):
+        yield
+
+
+def _on(device):
+    """Makes the tensors' device the current one for a call (the library
+    launches there); nothing to do where it is."""
+    return _NOTHING if device.index == torch.cuda.current_device() else _other_device(device)
+
+
+_NOTHING = contextlib.nullcontext()
+
+
+def _row_stride(t: torch.Tensor, name: str, dtype, rows: int, cols: int, device) -> int:
+    """Elements from row to row of a [rows, cols] CUDA tensor whose rows are
+    contiguous (a column slice of a wider tensor may be passed)."""
+    if t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must be a {dtype} [{rows}, {cols}] tensor")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on the device of the others")
+    stride, inner = t.stride()
+    if inner != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return stride if rows > 1 else cols
+
+
+def _row_index(t: torch.Tensor, name: str, rows: int, device) -> int:
+    if t.dtype != torch.int32 or t.device != device or t.numel() != rows or not t.is_contiguous():
+        raise ValueError(f"{name} must hold one int32 per row, on the device of the others")
+    return t.data_ptr()
+
+
+@dataclass(slots=True)
+class Norm:
+    """A norm over the columns: kind "rms" or "layer", optional weight and bias."""
+    kind: str = "rms"
+    weight: torch.Tensor | None = None
+    bias: torch.Tensor | None = None
+    eps: float = 1e-6
+
+
+_NORM_KINDS = {"rms": 1, "layer": 2}      # nvfp4_norm values
+_DTYPES = {torch.bfloat16: 0, torch.float32: 1}  # nvfp4_dtype values
+
+
+class ResidualNorm(NamedTuple):
+    """Results of residual_norm; what was not asked for is None."""
+    h: torch.Tensor | None
+    out: torch.Tensor | None
+    quant: NVFP4Tensor | None
+
+
+def residual_norm(residual: torch.Tensor, y: torch.Tensor | None = None, *,
+                  post: Norm | None = None, gate: torch.Tensor | None = None,
+                  pre: Norm | None = None, scale: torch.Tensor | None = None,
+                  shift: torch.Tensor | None = None, row_group: torch.Tensor | None = None,
+                  residual_scale: float = 1.0, branch_scale: float = 1.0,
+                  h: torch.Tensor | None = None, want_h: bool = True,
+                  out: torch.Tensor | None = None, want_out: bool = True,
+                  quant: NVFP4Tensor | None = None, want_quant: bool = False,
+                  amax_rows: torch.Tensor | None = None, stream=None) -> ResidualNorm:
+    """The norms after one block and before the next, in one launch.  Per row,
+    with g the row's request:
+
+        h     = residual_scale * residual + branch_scale * gate[g] * post(y)
+        out   = pre(h) * (1 + scale[g]) + shift[g]
+        quant = quantize_rowwise(out)
+
+    residual: [rows, cols] bf16 or fp32 (h has its type); y: [rows, cols] bf16,
+    or None at the start of a model; cols a multiple of 16, at most 32768.
+    gate, scale, shift: [cols], or [groups, cols] with any row stride that is a
+    multiple of 8 (chunks of one modulation tensor).  row_group: int32 per row,
+    its request; rows with a negative number, or one not below groups where a
+    vector has groups, are padding, and their results are left as they were.
+    Without it each request has rows / groups consecutive rows.  Weights, biases, gate, scale and shift are all bf16 or
+    all fp32.  h, out and quant may be given; h may be the residual itself.
+    Without pre, only h is computed."""
+    if residual.dim() != 2 or residual.dtype not in _DTYPES:
+        raise ValueError("residual must be a bf16 or fp32 [rows, cols] tensor")
+    rows, cols = residual.shape
+    dev, bf16 = residual.device, torch.bfloat16
+    a = ResidualNormArgs()
+    a.rows, a.cols = rows, cols
+    a.residual_stride = _row_stride(residual, "residual", residual.dtype, rows, cols, dev)
+    a.residual = residual.data_ptr()
+    a.stream_dtype = _DTYPES[residual.dtype]
+    a.residual_scale, a.branch_scale = residual_scale, branch_scale
+    if y is not None:
+        a.y_stride = _row_stride(y, "y", bf16, rows, cols, dev)
+        a.y = y.data_ptr()
+        if h is None and want_h:
+            h = torch.empty(rows, cols, dtype=residual.dtype, device=dev)
+    elif post is not None or gate is not None or h is not None:
+        raise ValueError("post, gate and h need y")
+    if h is not None:
+        a.h_stride = _row_stride(h, "h", residual.dtype, rows, cols, dev)
+        a.h = h.data_ptr()
+    if pre is None:
+        if scale is not None or shift is not None or out is not None or quant is not None or want_quant:
+            raise ValueError("scale, shift, out and quant need pre")
+    else:
+        if out is None and want_out:
+            out = torch.empty(rows, cols, dtype=bf16, device=dev)
+        if out is not None:
+            a.out_stride = _row_stride(out, "out", bf16, rows, cols, dev)
+            a.out = out.data_ptr()
+        if quant is None and want_quant:
+            quant = empty_nvfp4(rows, cols, dev, row_scales=True)
+        if quant is not None:
+            if ((quant.rows, quant.cols) != (rows, cols) or quant.s_dec.numel() != rows or
+                    quant.q.device != dev or quant.q.numel() != rows * cols // 2):
+                raise ValueError("quant must be an NVFP4Tensor of these rows and columns with row scales")
+            a.q, a.sf, a.s_dec_rows = quant.q.data_ptr(), quant.sf.data_ptr(), quant.s_dec.data_ptr()
+    if amax_rows is not None:
+        if (quant is None or amax_rows.numel() != rows or amax_rows.dtype != torch.float32 or
+                amax_rows.device != dev or not amax_rows.is_contiguous()):
+            raise ValueError("amax_rows must hold one fp32 per row, and needs quant")
+        a.amax_rows = amax_rows.data_ptr()
+
+    vec_dtype, groups = None, 1
+
+    def vector(t, name):
+        nonlocal vec_dtype, groups
+        if t.dtype not in _DTYPES or (vec_dtype is not None and t.dtype != vec_dtype):
+            raise ValueError("weights, biases, gate, scale and shift must all be bf16 or all fp32")
+        vec_dtype = t.dtype
+        if t.device != dev or t.shape[-1] != cols or t.stride(-1) != 1:
+            raise ValueError(f"{name} must hold {cols} contiguous values, on the device of the others")
+        if t.dim() == 1:
+            return 0
+        if t.dim() != 2 or name.endswith(("weight", "bias")) or (groups not in (1, t.shape[0])):
+            raise ValueError(f"{name} must be [cols]" +
+                             ("" if name.endswith(("weight", "bias")) else " or [groups, cols], one groups for all"))
+        if t.shape[0] == 1:
+            return 0
+        groups = t.shape[0]
+        return t.stride(0)
+
+    for name, norm in (("post", post), ("pre", pre)):
+        if norm is None:
+            continue
+        if norm.kind not in _NORM_KINDS:
+            raise ValueError(f"{name}: a norm is 'rms' or 'layer'")
+        setattr(a, name + "_norm", _NORM_KINDS[norm.kind])
+        setattr(a, name + "_eps", norm.eps)
+        if norm.weight is not None:
+            vector(norm.weight, name + ".weight")
+            setattr(a, name + "_weight", norm.weight.data_ptr())
+        if norm.bias is not None:
+            vector(norm.bias, name + ".bias")
+            setattr(a, name + "_bias", norm.bias.data_ptr())
+    if gate is not None:
+        a.gate_stride = vector(gate, "gate")
+        a.gate = gate.data_ptr()
+    if scale is not None:
+        a.scale_stride = vector(scale, "scale")
+        a.scale = scale.data_ptr()
+    if shift is not None:
+        a.shift_stride = vector(shift, "shift")
+        a.shift = shift.data_ptr()
+    a.vector_dtype = _DTYPES[vec_dtype] if vec_dtype is not None else 0
+    a.groups = groups
+    if row_group is not None:
+        a.row_group = _row_index(row_group, "row_group", rows, dev)
+        if groups == 1:  # no vector of a request's own: every number from 0 on is one
+            a.groups = 1 << 31
+    with _on(dev):
+        _check("nvfp4_residual_norm",
+               lib().nvfp4_residual_norm(ctypes.byref(a), _raw_stream(dev, stream)))
+    return ResidualNorm(h, out, quant)
 
 
 def device_error() -> tuple[int, int]:
