@@ -343,6 +343,44 @@ typedef struct {
 /* One launch; see nvfp4_residual_norm_args. */
 nvfp4_status nvfp4_residual_norm(const nvfp4_residual_norm_args *args, nvfp4_stream_t stream);
 
+/* Arguments of nvfp4_lora: low-rank adapters of the requests in a batch,
+ * beside a projection that all of them share.  Row m with s = row_slot[m]:
+ *   out[m] = bf16(y[m] + scale[s] * B[s] (A[s] x[m]))
+ * with products, sums and the inner vector in fp32 (kept to 16 bits of
+ * mantissa at least), rounded once.  A row whose slot is not in [0, slots) has
+ * no adapter: out[m] = y[m].  Rows need no order; what one adapter holds
+ * (infinities, NaN) reaches no other adapter's rows.
+ *   rows, k, n   rows >= 0; k % 16 == 0, n % 8 == 0, both in [16, 2^20]
+ *   rank         16 .. 128, rank % 16 == 0 (pad smaller ones with zeros)
+ *   slots        adapters held, 1 <= slots, slots * max(k, n) < 2^31
+ *   x, y, out    device, bf16 [rows, k], [rows, n], [rows, n]; strides in
+ *                elements from row to row, a multiple of 8, at least k or n.
+ *                out may be y itself; otherwise it must not overlap the inputs.
+ *   a, b         device, bf16 [slots, rank, k] and [slots, n, rank], contiguous
+ *   scale        device, slots fp32
+ *   row_slot     device, rows int32, or NULL: slot 0 for every row
+ *   workspace    device, nvfp4_lora_workspace_bytes(rows, k, n, rank) bytes
+ *                (may be NULL where that is 0), overwritten; calls that share
+ *                one must be ordered */
+typedef struct {
+    int64_t rows, k, n, rank, slots;
+    const void *x;
+    int64_t x_stride;
+    const void *y;
+    int64_t y_stride;
+    void *out;
+    int64_t out_stride;
+    const void *a;
+    const void *b;
+    const float *scale;
+    const int32_t *row_slot;
+    void *workspace;
+} nvfp4_lora_args;
+
+size_t nvfp4_lora_workspace_bytes(int64_t rows, int64_t k, int64_t n, int64_t rank);
+
+nvfp4_status nvfp4_lora(const nvfp4_lora_args *args, nvfp4_stream_t stream);
+
 /* Failure-detection self-test (no counterpart on the pages): launches one
  * warp that waits, through the same bounded mbarrier wait every kernel of
  * this library uses, on a barrier that is never completed.  After

@@ -64,6 +64,13 @@ class ResidualNormArgs(ctypes.Structure):
                 [(n, ctypes.c_int) for n in ("post_norm", "pre_norm", "stream_dtype", "vector_dtype")])
 
 
+class LoraArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("rows", "k", "n", "rank", "slots")] +
+                [f for n in ("x", "y", "out")
+                 for f in ((n, ctypes.c_void_p), (n + "_stride", ctypes.c_int64))] +
+                [(n, ctypes.c_void_p) for n in ("a", "b", "scale", "row_slot", "workspace")])
+
+
 _lib = None
 
 
@@ -109,6 +116,10 @@ def lib() -> ctypes.CDLL:
         L.nvfp4_fp8_gemm.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, vp, vp]
         L.nvfp4_residual_norm.restype = st
         L.nvfp4_residual_norm.argtypes = [ctypes.POINTER(ResidualNormArgs), vp]
+        L.nvfp4_lora_workspace_bytes.restype = ctypes.c_size_t
+        L.nvfp4_lora_workspace_bytes.argtypes = [i64, i64, i64, i64]
+        L.nvfp4_lora.restype = st
+        L.nvfp4_lora.argtypes = [ctypes.POINTER(LoraArgs), vp]
         L.nvfp4_selftest_wait_timeout.restype = st
         L.nvfp4_selftest_wait_timeout.argtypes = [i64, vp]
         L.nvfp4_linear_host.restype = st
@@ -348,8 +359,19 @@ class FP8Linear:
         self.w = quantize_fp8(weight)
 
     def __call__(self, x: torch.Tensor, y: torch.Tensor | None = None,
-                 fused: FusedQuant | None = None, want_y: bool = True):
-        return gemm_fp8(quantize_fp8(x), self.w, y, fused, want_y)
+                 fused: FusedQuant | None = None, want_y: bool = True,
+                 adapters: LoraAdapters | None = None, row_slot: torch.Tensor | None = None):
+        _adapters_need_y(adapters, row_slot, y, fused, want_y)
+        y = gemm_fp8(quantize_fp8(x), self.w, y, fused, want_y)
+        return y if adapters is None else lora(x, y, adapters, row_slot, out=y)
+
+
+def _adapters_need_y(adapters, row_slot, y, fused, want_y) -> None:
+    if adapters is None:
+        if row_slot is not None:
+            raise ValueError("row_slot needs adapters")
+    elif fused is not None or (y is None and not want_y):
+        raise ValueError("adapters are added to the bf16 output: fused codes would miss them")
 
 
 SELFTEST_TAG = 90
@@ -365,7 +387,10 @@ def selftest_wait_timeout(timeout_us: int = 50_000, stream=None) -> None:
 class NVFP4Linear:
     """An nn.Linear-shaped NVFP4 layer: weights quantized once with a static
     per-tensor scale (from the weight amax, or a given one), activations
-    quantized dynamically on every call."""
+    quantized dynamically on every call.  adapters (with row_slot, one int32
+    per row) adds the low-rank adapters of the rows' requests to the output;
+    x may be given quantized already (xq, as residual_norm's quant), x itself
+    then being read by the adapters only."""
 
     def __init__(self, weight: torch.Tensor, w_amax: torch.Tensor | None = None):
         _require(weight, torch.bfloat16, "weight")
@@ -380,11 +405,18 @@ class NVFP4Linear:
                        torch.empty(1, dtype=torch.float32, device=device))
         return self._x
 
-    def __call__(self, x: torch.Tensor, y: torch.Tensor | None = None,
-                 fused: FusedQuant | None = None, want_y: bool = True) -> torch.Tensor | None:
-        xq, amax = self._xbuf(x.shape[0], x.device)
-        quantize_dynamic(x, xq, amax)
-        return gemm(xq, self.w, y, fused, want_y)
+    def __call__(self, x: torch.Tensor | None, y: torch.Tensor | None = None,
+                 fused: FusedQuant | None = None, want_y: bool = True, *,
+                 xq: NVFP4Tensor | None = None, adapters: LoraAdapters | None = None,
+                 row_slot: torch.Tensor | None = None) -> torch.Tensor | None:
+        _adapters_need_y(adapters, row_slot, y, fused, want_y)
+        if xq is None:
+            xq, amax = self._xbuf(x.shape[0], x.device)
+            quantize_dynamic(x, xq, amax)
+        elif x is None and adapters is not None:
+            raise ValueError("adapters need x in bf16")
+        y = gemm(xq, self.w, y, fused, want_y)
+        return y if adapters is None else lora(x, y, adapters, row_slot, out=y)
 
     def forward_host(self, x_host: torch.Tensor, y_host: torch.Tensor, ws: dict,
                      stream=None, single_launch: bool = True) -> None:
@@ -595,6 +627,86 @@ def residual_norm(residual: torch.Tensor, y: torch.Tensor | None = None, *,
         _check("nvfp4_residual_norm",
                lib().nvfp4_residual_norm(ctypes.byref(a), _raw_stream(dev, stream)))
     return ResidualNorm(h, out, quant)
+
+
+@dataclass(slots=True)
+class LoraAdapters:
+    """Low-rank adapters of one projection, held side by side: slot s adds
+    scale[s] * B[s] (A[s] x).  One rank for all, a multiple of 16 up to 128;
+    pack_adapters pads smaller ones."""
+    a: torch.Tensor      # bf16 [slots, rank, K]
+    b: torch.Tensor      # bf16 [slots, N, rank]
+    scale: torch.Tensor  # fp32 [slots]
+
+
+def pack_adapters(adapters, device=None) -> LoraAdapters:
+    """LoraAdapters from a list of (A [r, K], B [N, r], scale), whose ranks may
+    differ: each is padded with zeros to the largest one's next multiple of 16."""
+    if not adapters:
+        raise ValueError("pack_adapters needs at least one adapter")
+    k, n = adapters[0][0].shape[1], adapters[0][1].shape[0]
+    for a, b, _ in adapters:
+        if a.dim() != 2 or b.dim() != 2 or a.shape[1] != k or b.shape[0] != n or a.shape[0] != b.shape[1]:
+            raise ValueError("each adapter is (A [r, K], B [N, r], scale), with the same K and N for all")
+    rank = max(16, (max(a.shape[0] for a, _, _ in adapters) + 15) // 16 * 16)
+    if rank > 128:
+        raise ValueError("ranks up to 128 are supported")
+    dev = adapters[0][0].device if device is None else device
+    pa = torch.zeros(len(adapters), rank, k, dtype=torch.bfloat16, device=dev)
+    pb = torch.zeros(len(adapters), n, rank, dtype=torch.bfloat16, device=dev)
+    for i, (a, b, _) in enumerate(adapters):
+        pa[i, :a.shape[0]] = a
+        pb[i, :, :a.shape[0]] = b
+    scale = torch.tensor([float(s) for _, _, s in adapters], dtype=torch.float32, device=dev)
+    return LoraAdapters(pa, pb, scale)
+
+
+def lora(x: torch.Tensor, y: torch.Tensor, adapters: LoraAdapters,
+         row_slot: torch.Tensor | None = None, out: torch.Tensor | None = None,
+         workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """out[m] = y[m] + scale[s] * B[s] (A[s] x[m]) with s = row_slot[m], the
+    low-rank adapters of many requests beside a projection y they share.
+
+    x: [rows, K] and y: [rows, N], bf16 (K % 16 == 0, N % 8 == 0; rows may be
+    strided by a multiple of 8 elements).  row_slot: int32 per row, in any
+    order; a number outside [0, slots) means no adapter (out = y).  None: slot 0
+    for every row.  out may be y itself; a new tensor if not given."""
+    a, b, scale = adapters.a, adapters.b, adapters.scale
+    if a.dim() != 3 or b.dim() != 3:
+        raise ValueError("adapters.a is [slots, rank, K], adapters.b [slots, N, rank]")
+    slots, rank, k = a.shape
+    n, dev, bf16 = b.shape[1], x.device, torch.bfloat16
+    if (a.dtype != bf16 or b.dtype != bf16 or scale.dtype != torch.float32 or
+            not (a.is_contiguous() and b.is_contiguous() and scale.is_contiguous()) or
+            b.shape[0] != slots or b.shape[2] != rank or scale.numel() != slots or
+            a.device != dev or b.device != dev or scale.device != dev):
+        raise ValueError("adapters must be contiguous bf16 a [slots, rank, K] and b [slots, N, rank] "
+                         "and fp32 scale [slots], on the device of x")
+    rows = x.shape[0]
+    p = LoraArgs()
+    p.rows, p.k, p.n, p.rank, p.slots = rows, k, n, rank, slots
+    p.x_stride = _row_stride(x, "x", bf16, rows, k, dev)
+    p.y_stride = _row_stride(y, "y", bf16, rows, n, dev)
+    if out is None:
+        out = torch.empty(rows, n, dtype=bf16, device=dev)
+    p.out_stride = _row_stride(out, "out", bf16, rows, n, dev)
+    p.x, p.y, p.out = x.data_ptr(), y.data_ptr(), out.data_ptr()
+    p.a, p.b, p.scale = a.data_ptr(), b.data_ptr(), scale.data_ptr()
+    if row_slot is not None:
+        p.row_slot = _row_index(row_slot, "row_slot", rows, dev)
+    with _on(dev):
+        need = lib().nvfp4_lora_workspace_bytes(rows, k, n, rank)
+        if need:
+            if workspace is None:
+                # Of the stream it is used on, so that it is free again in that stream's order.
+                with torch.cuda.stream(stream):
+                    workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            elif workspace.device != dev or not workspace.is_contiguous() or \
+                    workspace.numel() * workspace.element_size() < need:
+                raise ValueError(f"workspace must hold {need} contiguous bytes on the device of x")
+            p.workspace = workspace.data_ptr()
+        _check("nvfp4_lora", lib().nvfp4_lora(ctypes.byref(p), _raw_stream(dev, stream)))
+    return out
 
 
 def device_error() -> tuple[int, int]:

@@ -31,6 +31,11 @@ bool norm_ok(int kind, float eps, const void *weight, const void *bias) {
     return std::isfinite(eps) && eps >= 0.0f;
 }
 
+bool lora_sizes_ok(int64_t rows, int64_t k, int64_t n, int64_t rank) {
+    return rows >= 0 && rows <= (int64_t(1) << 27) && k >= 16 && k <= (1 << 20) && k % 16 == 0 &&
+           n >= 16 && n <= (1 << 20) && n % 8 == 0 && rank >= 16 && rank <= 128 && rank % 16 == 0;
+}
+
 }  // namespace
 
 extern "C" {
@@ -84,6 +89,37 @@ nvfp4_status nvfp4_residual_norm(const nvfp4_residual_norm_args *args, nvfp4_str
     if (st != NVFP4_OK) return st;
     if (a.rows == 0) return NVFP4_OK;
     return nvfp4::launch_residual_norm(a, sms, stream) == cudaSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
+}
+
+size_t nvfp4_lora_workspace_bytes(int64_t rows, int64_t k, int64_t n, int64_t rank) {
+    if (!lora_sizes_ok(rows, k, n, rank)) return 0;
+    return nvfp4::lora_workspace_bytes(rows, k, n, rank);
+}
+
+nvfp4_status nvfp4_lora(const nvfp4_lora_args *args, nvfp4_stream_t stream) {
+    if (args == nullptr) return NVFP4_ERR_INVALID_ARG;
+    const nvfp4_lora_args &p = *args;
+    if (!lora_sizes_ok(p.rows, p.k, p.n, p.rank)) return NVFP4_ERR_INVALID_ARG;
+    if (p.slots < 1 || p.slots >= (int64_t(1) << 31) / (p.k > p.n ? p.k : p.n))
+        return NVFP4_ERR_INVALID_ARG;
+    if (p.a == nullptr || p.b == nullptr || p.scale == nullptr) return NVFP4_ERR_INVALID_ARG;
+    if (p.rows > 0 && (p.x == nullptr || p.y == nullptr || p.out == nullptr || p.out == p.x))
+        return NVFP4_ERR_INVALID_ARG;
+    if (!stride_ok(p.x_stride, p.rows, p.k) || !stride_ok(p.y_stride, p.rows, p.n) ||
+        !stride_ok(p.out_stride, p.rows, p.n))
+        return NVFP4_ERR_INVALID_ARG;
+    if (p.out == p.y && p.out_stride != p.y_stride) return NVFP4_ERR_INVALID_ARG;
+    const bool needs_workspace = nvfp4::lora_workspace_bytes(p.rows, p.k, p.n, p.rank) > 0;
+    if (needs_workspace && p.workspace == nullptr) return NVFP4_ERR_INVALID_ARG;
+    const void *wide[] = {p.x, p.y, p.out, p.a, p.b, p.workspace};
+    for (const void *q : wide)
+        if (!aligned(q, 16)) return NVFP4_ERR_MISALIGNED;
+    if (!aligned(p.scale, 4) || !aligned(p.row_slot, 4)) return NVFP4_ERR_MISALIGNED;
+    int sms = 0;
+    const nvfp4_status st = nvfp4::current_device(&sms);
+    if (st != NVFP4_OK) return st;
+    if (p.rows == 0) return NVFP4_OK;
+    return nvfp4::launch_lora(p, sms, stream) == cudaSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
 }
 
 }  // extern "C"

@@ -14,4 +14,10 @@ namespace nvfp4 {
 cudaError_t launch_residual_norm(const nvfp4_residual_norm_args &a, int num_sms,
                                  cudaStream_t stream);
 
+// Bytes of workspace of launch_lora (0 where it needs none).
+size_t lora_workspace_bytes(int64_t rows, int64_t k, int64_t n, int64_t rank);
+
+// A checked adapter call (see nvfp4_lora_args); rows > 0.
+cudaError_t launch_lora(const nvfp4_lora_args &p, int num_sms, cudaStream_t stream);
+
 }  // namespace nvfp4

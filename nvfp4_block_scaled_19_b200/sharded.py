@@ -16,7 +16,7 @@ from __future__ import annotations
 import torch
 import torch.distributed as dist
 
-from . import NVFP4Linear, NVFP4Tensor, gemm, quantize, tensor_amax
+from . import NVFP4Linear, NVFP4Tensor, quantize, tensor_amax
 
 
 def shard_rows(rows: int, world: int, rank: int) -> tuple[int, int]:
@@ -56,6 +56,7 @@ class ShardedNVFP4Linear:
         self.amax = torch.empty(1, dtype=torch.float32, device=w.device)
 
     def __call__(self, x_local: torch.Tensor, y: torch.Tensor | None = None, fused=None,
-                 want_y: bool = True) -> torch.Tensor | None:
+                 want_y: bool = True, adapters=None, row_slot=None) -> torch.Tensor | None:
+        """adapters and row_slot as for NVFP4Linear, row_slot for this rank's rows."""
         xq = quantize_sharded(x_local, amax=self.amax, group=self.group)
-        return gemm(xq, self.lin.w, y, fused, want_y)
+        return self.lin(x_local, y, fused, want_y, xq=xq, adapters=adapters, row_slot=row_slot)

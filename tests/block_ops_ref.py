@@ -74,3 +74,23 @@ def assert_close(got, ref, err, what=""):
     off = (got.double() - ref).abs()
     worst = float((off / bound).max()) if off.numel() else 0.0
     assert worst <= 1.0, f"{what}: {worst:.3f} times the bound"
+
+
+def lora64(x, y, adapters, row_slot):
+    """out and how far fp32 sums may be from it: a sum of K products, one of
+    rank, whatever their order, in steps of at most 16 products that are each
+    rounded (or cut off) to 24 bits, and an inner vector of at least 16 bits."""
+    out = y.double().clone()
+    err = torch.zeros_like(out)
+    slots, rank, k = adapters.a.shape
+    step = (k / 16 + rank / 16 + 64) * 2.0 ** -23 + 2.0 ** -16
+    slot = torch.zeros(x.shape[0], dtype=torch.int64, device=x.device) if row_slot is None else row_slot.long()
+    for s in range(slots):
+        rows = torch.nonzero(slot == s).reshape(-1)
+        if rows.numel() == 0:
+            continue
+        xd, a, b = x[rows].double(), adapters.a[s].double(), adapters.b[s].double()
+        c = adapters.scale[s].double()
+        out[rows] += c * (xd @ a.T) @ b.T
+        err[rows] = step * c.abs() * ((xd.abs() @ a.abs().T) @ b.abs().T) + 2.0 ** -23 * y[rows].double().abs()
+    return out, err

@@ -76,3 +76,48 @@ def test_accepted_arguments_reach_the_device_check(nv, p):
                dict(gate=p, gate_stride=0, scale=p, scale_stride=384, groups=2)):
         a = _norm_args(nv, p, **kw)
         assert nv.lib().nvfp4_residual_norm(ctypes.byref(a), None) == 3, kw
+
+
+def _lora_args(nv, p, **kw):
+    base = dict(rows=4, k=64, n=80, rank=16, slots=2, x=p, x_stride=64, y=p + 64, y_stride=80,
+                out=p + 128, out_stride=80, a=p, b=p, scale=p, workspace=p)
+    base.update(kw)
+    a = nv.LoraArgs()
+    for k, v in base.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("kw", [
+    dict(rows=-1), dict(rows=(1 << 27) + 1), dict(k=0), dict(k=72), dict(k=(1 << 20) + 16), dict(n=8), dict(n=84),
+    dict(n=(1 << 20) + 8), dict(rank=0), dict(rank=8), dict(rank=24), dict(rank=144), dict(slots=0),
+    dict(slots=1 << 25), dict(x=None), dict(y=None), dict(out=None), dict(a=None), dict(b=None), dict(scale=None),
+    dict(x_stride=56), dict(x_stride=68), dict(y_stride=72), dict(out_stride=0), dict(out_stride=1 << 59),
+], ids=str)
+def test_lora_invalid(nv, p, kw):
+    assert nv.lib().nvfp4_lora(ctypes.byref(_lora_args(nv, p, **kw)), None) == 1
+
+
+def test_lora_aliases_and_alignment(nv, p):
+    f = nv.lib().nvfp4_lora
+    assert f(None, None) == 1
+    assert f(ctypes.byref(_lora_args(nv, p, out=p)), None) == 1                       # out over x
+    assert f(ctypes.byref(_lora_args(nv, p, out=p + 64, out_stride=88)), None) == 1   # out over y, other rows
+    for name in ("x", "y", "out", "a", "b", "workspace"):
+        assert f(ctypes.byref(_lora_args(nv, p, **{name: p + 8})), None) == 2, name
+    for name in ("scale", "row_slot"):
+        assert f(ctypes.byref(_lora_args(nv, p, **{name: p + 2})), None) == 2, name
+
+
+def test_lora_workspace_sizes(nv):
+    f = nv.lib().nvfp4_lora_workspace_bytes
+    assert f(-1, 64, 64, 16) == 0 and f(4096, 72, 64, 16) == 0 and f(4096, 64, 64, 144) == 0
+    for rows in (0, 1, 100, 5000, 1 << 27):     # room for fp32 partial sums, or none
+        assert f(rows, 4096, 4096, 64) % (4 * 64) == 0
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-device answer")
+def test_lora_accepted_arguments_reach_the_device_check(nv, p):
+    for kw in (dict(), dict(rows=0, x=None, y=None, out=None), dict(row_slot=p), dict(out=p + 64),
+               dict(rows=1 << 16)):
+        assert nv.lib().nvfp4_lora(ctypes.byref(_lora_args(nv, p, **kw)), None) == 3, kw
