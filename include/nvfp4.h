@@ -352,7 +352,7 @@ nvfp4_status nvfp4_residual_norm(const nvfp4_residual_norm_args *args, nvfp4_str
  * (infinities, NaN) reaches no other adapter's rows.
  *   rows, k, n   rows >= 0; k % 16 == 0, n % 8 == 0, both in [16, 2^20]
  *   rank         16 .. 128, rank % 16 == 0 (pad smaller ones with zeros)
- *   slots        adapters held, 1 <= slots, slots * max(k, n) < 2^31
+ *   slots        adapters held, 1 <= slots, slots * max(k, n, rank) < 2^31
  *   x, y, out    device, bf16 [rows, k], [rows, n], [rows, n]; strides in
  *                elements from row to row, a multiple of 8, at least k or n.
  *                out may be y itself; otherwise it must not overlap the inputs.

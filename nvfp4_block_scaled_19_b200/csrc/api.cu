@@ -63,15 +63,6 @@ nvfp4_status current_device(int *num_sms) {
     return NVFP4_OK;
 }
 
-}  // namespace nvfp4
-
-namespace {
-
-using nvfp4::current_device;
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-nvfp4_status from_cuda(cudaError_t e) { return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH; }
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     // Looked up once; atomic because host threads may make their first calls
@@ -92,6 +83,17 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     }
     return fn;
 }
+
+}  // namespace nvfp4
+
+namespace {
+
+using nvfp4::current_device;
+using nvfp4::tensor_map_encoder;
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+nvfp4_status from_cuda(cudaError_t e) { return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH; }
 
 // 2-D byte tensor [rows, row_bytes] (row-major), 128-byte-swizzled boxes of
 // box_rows x 128 bytes.

@@ -2,6 +2,9 @@
 // entry point refuses a bad call in the same way and before any device work.
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <cstdint>
 
 #include "nvfp4.h"
@@ -17,5 +20,8 @@ nvfp4_status check_quantize_args(const void *x, int64_t rows, int64_t cols, cons
 // The current device, if it can run this library's sm_100a kernels
 // (compute capability 10.0); its SM count in *num_sms.
 nvfp4_status current_device(int *num_sms);
+
+// The driver's tensor-map encoder, looked up once (nullptr where there is none).
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 }  // namespace nvfp4

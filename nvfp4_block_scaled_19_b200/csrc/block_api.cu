@@ -100,7 +100,8 @@ nvfp4_status nvfp4_lora(const nvfp4_lora_args *args, nvfp4_stream_t stream) {
     if (args == nullptr) return NVFP4_ERR_INVALID_ARG;
     const nvfp4_lora_args &p = *args;
     if (!lora_sizes_ok(p.rows, p.k, p.n, p.rank)) return NVFP4_ERR_INVALID_ARG;
-    if (p.slots < 1 || p.slots >= (int64_t(1) << 31) / (p.k > p.n ? p.k : p.n))
+    const int64_t widest = p.k > p.n ? p.k : p.n;
+    if (p.slots < 1 || p.slots >= (int64_t(1) << 31) / (widest > p.rank ? widest : p.rank))
         return NVFP4_ERR_INVALID_ARG;
     if (p.a == nullptr || p.b == nullptr || p.scale == nullptr) return NVFP4_ERR_INVALID_ARG;
     if (p.rows > 0 && (p.x == nullptr || p.y == nullptr || p.out == nullptr || p.out == p.x))
@@ -119,7 +120,7 @@ nvfp4_status nvfp4_lora(const nvfp4_lora_args *args, nvfp4_stream_t stream) {
     const nvfp4_status st = nvfp4::current_device(&sms);
     if (st != NVFP4_OK) return st;
     if (p.rows == 0) return NVFP4_OK;
-    return nvfp4::launch_lora(p, sms, stream) == cudaSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
+    return nvfp4::launch_lora(p, stream) == cudaSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
 }
 
 }  // extern "C"

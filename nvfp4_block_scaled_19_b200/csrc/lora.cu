@@ -160,13 +160,16 @@ __global__ void __launch_bounds__(kRowThreads) __cluster_dims__(kCluster, 1, 1)
 
 }  // namespace
 
+// Rows from which the tiles are taken.
+constexpr int64_t kTileFromRows = 97;
+
 size_t lora_workspace_bytes(int64_t rows, int64_t k, int64_t n, int64_t rank) {
-    (void)rows; (void)k; (void)n; (void)rank;
-    return 0;
+    (void)n;
+    return rows < kTileFromRows ? 0 : lora_tile_workspace_bytes(rows, k, rank);
 }
 
-cudaError_t launch_lora(const nvfp4_lora_args &p, int num_sms, cudaStream_t stream) {
-    (void)num_sms;
+cudaError_t launch_lora(const nvfp4_lora_args &p, cudaStream_t stream) {
+    if (p.rows >= kTileFromRows) return launch_lora_tile(p, stream);
     lora_rows_kernel<<<static_cast<unsigned>(p.rows * kCluster), kRowThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }

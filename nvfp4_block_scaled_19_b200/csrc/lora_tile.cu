@@ -1,0 +1,814 @@
+// Low-rank adapters for many rows (the mathematics is stated in lora.cu): two
+// launches on 128-row tiles, both tcgen05 with TMA-fed shared memory.
+//
+// lora_shrink_kernel   partial[sp][m][:] = A[s] x[m] over the K range of split sp.
+//   Item = (row tile, split).  A stage is the tile's 128 x 64 piece of x and,
+//   side by side as one B operand, the matching rank x 64 pieces of up to
+//   G = NB / rank different adapters, so a tile whose rows belong to G requests
+//   still reads x once; each row's epilogue thread keeps its own adapter's
+//   columns.  x is split over K when the row tiles alone leave SMs idle; the
+//   partial sums are added in a fixed order by the next launch, so the
+//   result does not depend on timing.
+// lora_expand_kernel   out[m][n] = bf16(y[m][n] + B[s] t[m]),
+//   t[m] = scale[s] * sum_sp partial[sp][m].
+//   A CTA keeps t of its row tile in shared memory and walks over units of 64
+//   columns: y by TMA into a ring, B's 64 x rank piece by TMA, the product in
+//   tensor memory, added to y in place in the ring, out by TMA.  t is kept as
+//   the sum of two bf16 (hi + lo, 16 mantissa bits), two MMAs per 16 ranks, so
+//   the product keeps nearly fp32 accuracy while B, which is bf16 already,
+//   needs no second copy.  A tile with rows of several adapters makes one
+//   product per adapter, each row taking its own adapter's: nothing of another
+//   adapter, not even NaN, reaches a row.
+//
+// What bounds them: HBM (x once; y and out once).  Rank 128 is 64 flops per byte
+// of x, above what the register-operand MMAs sustain beside the loads and far
+// below tcgen05's rate.
+//
+// Roles of both: warp 0 TMA producer, warp 1 MMA issuer (and tensor memory),
+// warps 2-5 epilogue (one 32-lane quadrant each).  Every wait is bounded; on a
+// timeout the kernel records NVFP4_ERR_TIMEOUT (tags 40-47), all roles stop,
+// copies and MMAs in flight are drained with bounded waits and tensor memory is
+// freed.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+#include <cstring>
+
+#include "api_checks.h"
+#include "block_ops.h"
+#include "gemm.h"
+#include "nvfp4_math.cuh"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kTileRows = 128;
+constexpr int kThreads = 192;
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr uint32_t kXBytes = kTileRows * 128;  // 128 rows x 64 bf16
+constexpr uint32_t kUnitCols = 64;
+
+// ---------------------------------------------------------------- PTX
+
+__device__ __forceinline__ uint32_t s32(const void *p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+__device__ __forceinline__ uint64_t timer_ns() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
+}
+
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// Where a wait that gives up says so.
+struct Abort {
+    volatile int *flag;  // shared, seen by every role
+    int *err;            // the library's device error word
+};
+
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const Abort &ab, int tag) {
+    if (bar_try(bar, parity)) return true;
+    const uint64_t t0 = timer_ns();
+    while (true) {
+        if (bar_try(bar, parity)) return true;
+        if (*ab.flag) return false;
+        if (timer_ns() - t0 > kTimeoutNs) {
+            if (atomicCAS(&ab.err[0], 0, NVFP4_ERR_TIMEOUT) == 0) ab.err[1] = tag;
+            *ab.flag = 1;
+            return false;
+        }
+    }
+}
+
+// The same by a whole warp: lane 0 polls, so the warp cannot part.
+__device__ __forceinline__ bool bar_wait_warp(uint32_t bar, uint32_t parity, const Abort &ab, int tag) {
+    int ok = 0;
+    if ((threadIdx.x & 31) == 0) ok = bar_wait(bar, parity, ab, tag) ? 1 : 0;
+    return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
+}
+
+// On the way out after a timeout: waits for copies or MMAs in flight, bounded.
+__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity, uint64_t deadline) {
+    while (!bar_try(bar, parity))
+        if (timer_ns() > deadline) return;
+}
+
+__device__ __forceinline__ void load_2d(const CUtensorMap *m, uint32_t bar, uint32_t dst, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(m), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+
+__device__ __forceinline__ void store_2d(const CUtensorMap *m, uint32_t src, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(m),
+        "r"(src), "r"(x), "r"(y)
+        : "memory");
+}
+
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
+    // K-major, 128-byte swizzle: 8-row groups of 1024 bytes.
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFF) | (1ull << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// kind::f16 with bf16 operands, both K-major, fp32 accumulator.
+__device__ __forceinline__ uint32_t bf16_idesc(int n) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(kTileRows >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void fence_before() {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+
+__device__ __forceinline__ void fence_after() {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+// 16 columns of this warp's 32 lanes, complete on return.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&f)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32"
+        " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ uint4 ld_shared_16B(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void st_shared_16B(uint32_t a, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
+                 "r"(v.w)
+                 : "memory");
+}
+
+// ---------------------------------------------------------------- the tile's adapters
+
+struct TileSlots {
+    int row[kTileRows];       // each row's adapter, as its place in `list`, or -1
+    int list[kTileRows];      // the different adapters, in order of first use
+    int count;
+    int warp_count[4];
+};
+
+// Fills `ts` for rows [m0, m0 + 128) (all threads call; ends with a barrier).
+__device__ __forceinline__ void find_slots(TileSlots &ts, const nvfp4_lora_args &p, int64_t m0) {
+    const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
+    int slot = -1;
+    if (i < kTileRows) {
+        if (m0 + i < p.rows) {
+            slot = p.row_slot != nullptr ? __ldg(p.row_slot + m0 + i) : 0;
+            if (slot < 0 || slot >= p.slots) slot = -1;
+        }
+        ts.row[i] = slot;
+    }
+    __syncthreads();
+    bool first = false;
+    unsigned firsts = 0;
+    if (i < kTileRows) {
+        const unsigned same = __match_any_sync(0xFFFFFFFFu, slot);
+        first = slot >= 0 && lane == __ffs(same) - 1;
+        if (first)
+            for (int j = 0; j < 32 * warp; ++j) first = first && ts.row[j] != slot;
+        __syncwarp();
+        firsts = __ballot_sync(0xFFFFFFFFu, first);
+        if (lane == 0) ts.warp_count[warp] = __popc(firsts);
+    }
+    __syncthreads();
+    if (i < kTileRows) {
+        int at = __popc(firsts & ((1u << lane) - 1u));
+        for (int w = 0; w < warp; ++w) at += ts.warp_count[w];
+        if (first) ts.list[at] = slot;
+        if (i == 0) ts.count = ts.warp_count[0] + ts.warp_count[1] + ts.warp_count[2] + ts.warp_count[3];
+    }
+    __syncthreads();
+    if (i < kTileRows && slot >= 0) {
+        int d = 0;
+        while (ts.list[d] != slot) ++d;  // it is in the list
+        ts.row[i] = d;
+    }
+    __syncthreads();
+}
+
+struct alignas(64) ShrinkMaps {
+    CUtensorMap x, a;
+};
+
+struct alignas(64) ExpandMaps {
+    CUtensorMap y, b, out;
+};
+
+// ---------------------------------------------------------------- shrink
+
+template <int NB>
+struct ShrinkConfig {
+    static constexpr int STAGES = NB == 64 ? 4 : 3;  // two CTAs of ~96 KB per SM
+    static constexpr uint32_t STAGE_BYTES = kXBytes + NB * 128;
+    static constexpr uint32_t SMEM_BYTES = STAGES * STAGE_BYTES + 1024;
+    static constexpr uint32_t TMEM_COLS = 2 * NB;  // two accumulators
+};
+
+template <int NB>
+__global__ void __launch_bounds__(kThreads)
+    lora_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const nvfp4_lora_args p,
+                       const int splits, float *__restrict__ partial, int *err) {
+    using Cfg = ShrinkConfig<NB>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ TileSlots ts;
+    __shared__ __align__(8) uint64_t bars[2 * Cfg::STAGES + 5];
+    __shared__ uint32_t tmem_holder;
+    __shared__ int abort_flag;
+    const uint32_t ring = (s32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t full = s32(bars), empty = full + 8 * Cfg::STAGES;
+    const uint32_t acc_full = empty + 8 * Cfg::STAGES, acc_empty = acc_full + 16, drain = acc_empty + 16;
+    const Abort ab{&abort_flag, err};
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tile = blockIdx.x / splits, split = blockIdx.x % splits;
+    const int64_t m0 = int64_t(tile) * kTileRows;
+    const int rank = static_cast<int>(p.rank);
+    const int k_blocks = static_cast<int>((p.k + 63) / 64);
+    const int kb0 = static_cast<int>(int64_t(k_blocks) * split / splits);
+    const int kb1 = static_cast<int>(int64_t(k_blocks) * (split + 1) / splits);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < Cfg::STAGES; ++s) {
+            bar_init(full + 8 * s, 1);
+            bar_init(empty + 8 * s, 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            bar_init(acc_full + 8 * s, 1);
+            bar_init(acc_empty + 8 * s, 4);
+        }
+        bar_init(drain, 1);
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    find_slots(ts, p, m0);
+    if (ts.count == 0) return;  // no row has an adapter
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         s32(&tmem_holder)),
+                     "r"(Cfg::TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = tmem_holder;
+    const int group = NB / rank;  // adapters per pass over x
+    const int passes = (ts.count + group - 1) / group;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0, issued = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int q = 0; q < passes && ok; ++q) {
+                const int d0 = q * group, d1 = min(ts.count, d0 + group);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!bar_wait(empty + 8 * stage, phase ^ 1, ab, 40)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t dst = ring + stage * Cfg::STAGE_BYTES, bar = full + 8 * stage;
+                    bar_expect(bar, kXBytes + (d1 - d0) * rank * 128);
+                    load_2d(&maps.x, bar, dst, kb * 64, static_cast<int>(m0));
+                    for (int d = d0; d < d1; ++d)
+                        load_2d(&maps.a, bar, dst + kXBytes + (d - d0) * rank * 128, kb * 64,
+                                ts.list[d] * rank);
+                    if (issued < Cfg::STAGES) ++issued;
+                    if (++stage == Cfg::STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            if (!ok) {
+                const uint64_t deadline = timer_ns() + kTimeoutNs;
+                for (int i = 0; i < issued; ++i) {
+                    if (--stage < 0) {
+                        stage = Cfg::STAGES - 1;
+                        phase ^= 1;
+                    }
+                    bar_drain(full + 8 * stage, phase, deadline);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int q = 0; q < passes && ok; ++q) {
+                const int d0 = q * group, d1 = min(ts.count, d0 + group);
+                const uint32_t idesc = bf16_idesc((d1 - d0) * rank);
+                const uint32_t acc = tmem + (q & 1) * NB;
+                if (!bar_wait(acc_empty + 8 * (q & 1), ((q >> 1) & 1) ^ 1, ab, 41)) {
+                    ok = false;
+                    break;
+                }
+                fence_after();
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!bar_wait(full + 8 * stage, phase, ab, 42)) {
+                        ok = false;
+                        break;
+                    }
+                    fence_after();
+                    const uint64_t a = operand_desc(ring + stage * Cfg::STAGE_BYTES);
+                    const uint64_t b = operand_desc(ring + stage * Cfg::STAGE_BYTES + kXBytes);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mma_bf16(acc, a + 2 * j, b + 2 * j, idesc, (kb > kb0 || j > 0) ? 1u : 0u);
+                    mma_commit(empty + 8 * stage);
+                    if (++stage == Cfg::STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (ok) mma_commit(acc_full + 8 * (q & 1));
+            }
+            mma_commit(drain);
+        }
+        __syncwarp();
+    } else {
+        const int quad = warp & 3, row = quad * 32 + lane;
+        const int mine = ts.row[row];
+        float *dst = partial + (int64_t(split) * p.rows + m0 + row) * rank;
+        for (int q = 0; q < passes; ++q) {
+            const int d0 = q * group, d1 = min(ts.count, d0 + group);
+            if (!bar_wait_warp(acc_full + 8 * (q & 1), (q >> 1) & 1, ab, 43)) break;
+            fence_after();
+            const uint32_t acc = tmem + (q & 1) * NB + (static_cast<uint32_t>(quad * 32) << 16);
+            for (int d = d0; d < d1; ++d)
+                for (int r = 0; r < rank; r += 16) {
+                    float f[16];
+                    __syncwarp();
+                    tmem_ld16(acc + (d - d0) * rank + r, f);
+                    if (mine == d) {  // also false for rows past the last one
+                        float4 *o = reinterpret_cast<float4 *>(dst + r);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            o[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+                    }
+                }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(acc_empty + 8 * (q & 1));
+        }
+    }
+    __syncthreads();
+    if (warp == 1) {
+        if (lane == 0) bar_drain(drain, 0, timer_ns() + kTimeoutNs);  // every MMA has completed
+        __syncwarp();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(Cfg::TMEM_COLS)
+                     : "memory");
+    }
+}
+
+// ---------------------------------------------------------------- expand
+
+// Shared-memory plan of one expand launch, made on the host from the rank.
+struct ExpandPlan {
+    int y_slots, b_slots;     // ring depths
+    uint32_t b_bytes;         // one B piece: 64 rows x (64 ranks x chunks)
+    uint32_t lo_offset;       // from t's hi part to its lo part
+    uint32_t t_bytes;
+    int chunks;               // 64-rank chunks
+    uint32_t smem_bytes;
+};
+
+constexpr int kMaxYSlots = 6, kMaxBSlots = 4;
+constexpr uint32_t kYBytes = kTileRows * 128;  // 128 rows x 64 columns
+constexpr int kAccs = 4;                       // accumulators of 64 columns
+
+ExpandPlan expand_plan(int64_t rank) {
+    ExpandPlan e;
+    e.chunks = rank > 64 ? 2 : 1;
+    e.b_bytes = e.chunks * 64 * 128;
+    // Up to rank 32, hi and lo share one 128-byte row.
+    e.lo_offset = rank <= 32 ? 64 : e.chunks * kTileRows * 128;
+    e.t_bytes = (rank <= 32 ? 1 : 2 * e.chunks) * kTileRows * 128;
+    // Two CTAs per SM up to rank 64 (at most 113 KB each), one above.
+    e.y_slots = rank <= 32 ? 4 : rank <= 64 ? 3 : 5;
+    e.b_slots = rank <= 64 ? 3 : 4;
+    e.smem_bytes = e.t_bytes + e.y_slots * kYBytes + e.b_slots * e.b_bytes + 1024;
+    return e;
+}
+
+__global__ void __launch_bounds__(kThreads)
+    lora_expand_kernel(const __grid_constant__ ExpandMaps maps, const nvfp4_lora_args p,
+                       const ExpandPlan plan, const int splits, const int ranges,
+                       const float *__restrict__ partial, int *err) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ TileSlots ts;
+    __shared__ __align__(8) uint64_t bars[2 * kMaxYSlots + 2 * kMaxBSlots + 2 * kAccs + 1];
+    __shared__ uint32_t tmem_holder;
+    __shared__ int abort_flag;
+    const uint32_t t_base = (s32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t y_ring = t_base + plan.t_bytes, b_ring = y_ring + plan.y_slots * kYBytes;
+    const uint32_t y_full = s32(bars), y_empty = y_full + 8 * kMaxYSlots;
+    const uint32_t b_full = y_empty + 8 * kMaxYSlots, b_empty = b_full + 8 * kMaxBSlots;
+    const uint32_t d_full = b_empty + 8 * kMaxBSlots, d_empty = d_full + 8 * kAccs;
+    const uint32_t drain = d_empty + 8 * kAccs;
+    const Abort ab{&abort_flag, err};
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tile = blockIdx.x / ranges, range = blockIdx.x % ranges;
+    const int64_t m0 = int64_t(tile) * kTileRows;
+    const int rank = static_cast<int>(p.rank);
+    const int units = static_cast<int>((p.n + kUnitCols - 1) / kUnitCols);
+    const int u0 = static_cast<int>(int64_t(units) * range / ranges);
+    const int u1 = static_cast<int>(int64_t(units) * (range + 1) / ranges);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < plan.y_slots; ++s) {
+            bar_init(y_full + 8 * s, 1);
+            bar_init(y_empty + 8 * s, 4);
+        }
+        for (int s = 0; s < plan.b_slots; ++s) {
+            bar_init(b_full + 8 * s, 1);
+            bar_init(b_empty + 8 * s, 1);
+        }
+        for (int s = 0; s < kAccs; ++s) {
+            bar_init(d_full + 8 * s, 1);
+            bar_init(d_empty + 8 * s, 4);
+        }
+        bar_init(drain, 1);
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    find_slots(ts, p, m0);
+    if (ts.count == 0 && p.out == p.y) return;  // nothing to add and nothing to copy
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         s32(&tmem_holder)),
+                     "r"(kAccs * kUnitCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    // t of the tile's rows: eight ranks per thread at a time.
+    if (ts.count > 0) {
+        const int groups = rank >> 3;
+        for (int i = threadIdx.x; i < kTileRows * groups; i += kThreads) {
+            const int row = i / groups, r = (i % groups) * 8;
+            float t[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) t[j] = 0.0f;
+            const int d = ts.row[row];
+            if (d >= 0) {
+                const float *src = partial + (m0 + row) * rank + r;
+                for (int s = 0; s < splits; ++s, src += p.rows * rank) {
+                    const float4 a = *reinterpret_cast<const float4 *>(src);
+                    const float4 b = *reinterpret_cast<const float4 *>(src + 4);
+                    t[0] += a.x; t[1] += a.y; t[2] += a.z; t[3] += a.w;
+                    t[4] += b.x; t[5] += b.y; t[6] += b.z; t[7] += b.w;
+                }
+                const float c = __ldg(p.scale + ts.list[d]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) t[j] *= c;
+            }
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(t[2 * j], t[2 * j + 1]);
+                const float2 back = __bfloat1622float2(h);
+                // An infinite (or NaN) value is carried by hi alone.
+                const float l0 = isfinite(back.x) ? t[2 * j] - back.x : 0.0f;
+                const float l1 = isfinite(back.y) ? t[2 * j + 1] - back.y : 0.0f;
+                const __nv_bfloat162 l = __floats2bfloat162_rn(l0, l1);
+                hi[j] = *reinterpret_cast<const uint32_t *>(&h);
+                lo[j] = *reinterpret_cast<const uint32_t *>(&l);
+            }
+            const uint32_t at = t_base + (r >> 6) * (kTileRows * 128) + row * 128;
+            const uint32_t col = (r & 63) * 2;  // bytes in the 128-byte row
+            const uint32_t lo_col = plan.lo_offset == 64 ? col + 64 : col;
+            const uint32_t lo_at = plan.lo_offset == 64 ? at : at + plan.lo_offset;
+            const uint32_t swz = (row & 7) << 4;
+            st_shared_16B(at + (col ^ swz), make_uint4(hi[0], hi[1], hi[2], hi[3]));
+            st_shared_16B(lo_at + (lo_col ^ swz), make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = tmem_holder;
+    const int count = ts.count;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int ys = 0, bs = 0, y_issued = 0, b_issued = 0;
+            uint32_t yph = 0, bph = 0;
+            bool ok = true;
+            for (int u = u0; u < u1 && ok; ++u) {
+                if (!bar_wait(y_empty + 8 * ys, yph ^ 1, ab, 44)) {
+                    ok = false;
+                    break;
+                }
+                bar_expect(y_full + 8 * ys, kYBytes);
+                load_2d(&maps.y, y_full + 8 * ys, y_ring + ys * kYBytes, u * kUnitCols,
+                        static_cast<int>(m0));
+                if (y_issued < plan.y_slots) ++y_issued;
+                if (++ys == plan.y_slots) {
+                    ys = 0;
+                    yph ^= 1;
+                }
+                for (int d = 0; d < count; ++d) {
+                    if (!bar_wait(b_empty + 8 * bs, bph ^ 1, ab, 45)) {
+                        ok = false;
+                        break;
+                    }
+                    bar_expect(b_full + 8 * bs, plan.b_bytes);
+                    const int row = static_cast<int>(ts.list[d] * p.n + u * kUnitCols);
+                    for (int c = 0; c < plan.chunks; ++c)
+                        load_2d(&maps.b, b_full + 8 * bs, b_ring + bs * plan.b_bytes + c * 8192, c * 64,
+                                row);
+                    if (b_issued < plan.b_slots) ++b_issued;
+                    if (++bs == plan.b_slots) {
+                        bs = 0;
+                        bph ^= 1;
+                    }
+                }
+            }
+            if (!ok) {
+                const uint64_t deadline = timer_ns() + kTimeoutNs;
+                for (int i = 0; i < y_issued; ++i) {
+                    if (--ys < 0) {
+                        ys = plan.y_slots - 1;
+                        yph ^= 1;
+                    }
+                    bar_drain(y_full + 8 * ys, yph, deadline);
+                }
+                for (int i = 0; i < b_issued; ++i) {
+                    if (--bs < 0) {
+                        bs = plan.b_slots - 1;
+                        bph ^= 1;
+                    }
+                    bar_drain(b_full + 8 * bs, bph, deadline);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = bf16_idesc(kUnitCols);
+            int bs = 0, acc = 0;
+            uint32_t bph = 0, aph = 0;
+            const int64_t total = int64_t(u1 - u0) * count;
+            for (int64_t i = 0; i < total; ++i) {
+                if (!bar_wait(b_full + 8 * bs, bph, ab, 46)) break;
+                if (!bar_wait(d_empty + 8 * acc, aph ^ 1, ab, 46)) break;
+                fence_after();
+                const uint32_t d = tmem + acc * kUnitCols;
+                for (int r = 0; r < rank; r += 16) {
+                    const uint32_t chunk = r >> 6, in = (r & 63) * 2;
+                    const uint64_t hi = operand_desc(t_base + chunk * (kTileRows * 128) + in);
+                    const uint64_t b = operand_desc(b_ring + bs * plan.b_bytes + chunk * 8192 + in);
+                    mma_bf16(d, hi, b, idesc, r > 0 ? 1u : 0u);
+                    mma_bf16(d, hi + (plan.lo_offset >> 4), b, idesc, 1u);
+                }
+                mma_commit(b_empty + 8 * bs);
+                mma_commit(d_full + 8 * acc);
+                if (++bs == plan.b_slots) {
+                    bs = 0;
+                    bph ^= 1;
+                }
+                if (++acc == kAccs) {
+                    acc = 0;
+                    aph ^= 1;
+                }
+            }
+            mma_commit(drain);
+        }
+        __syncwarp();
+    } else {
+        const int quad = warp & 3, row = quad * 32 + lane;
+        const int mine = ts.row[row];
+        const uint32_t swz = (row & 7) << 4;
+        const bool stored = m0 + quad * 32 < p.rows;  // a box of this warp's rows
+        int ys = 0, acc = 0, prev = -1;
+        uint32_t yph = 0, aph = 0;
+        bool ok = true;
+        for (int u = u0; u < u1 && ok; ++u) {
+            if (!bar_wait_warp(y_full + 8 * ys, yph, ab, 47)) break;
+            const uint32_t y = y_ring + ys * kYBytes + row * 128;
+            for (int d = 0; d < count; ++d) {
+                if (!bar_wait_warp(d_full + 8 * acc, aph, ab, 47)) {
+                    ok = false;
+                    break;
+                }
+                fence_after();
+                const uint32_t src = tmem + acc * kUnitCols + (static_cast<uint32_t>(quad * 32) << 16);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float f[16];
+                    __syncwarp();
+                    tmem_ld16(src + 16 * c, f);
+                    if (c == 3) {  // the accumulator is read: back to the MMA thread
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(d_empty + 8 * acc);
+                    }
+                    if (mine == d) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t at = y + ((32 * c + 16 * h) ^ swz);
+                            uint4 v = ld_shared_16B(at);
+                            uint32_t *w = &v.x;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const __nv_bfloat162 o =
+                                    __floats2bfloat162_rn(bf16_lo(w[j]) + f[8 * h + 2 * j],
+                                                          bf16_hi(w[j]) + f[8 * h + 2 * j + 1]);
+                                w[j] = *reinterpret_cast<const uint32_t *>(&o);
+                            }
+                            st_shared_16B(at, v);
+                        }
+                    }
+                }
+                if (++acc == kAccs) {
+                    acc = 0;
+                    aph ^= 1;
+                }
+            }
+            if (!ok) break;
+            // This warp's 32 rows go out; the slot of the unit before is free
+            // once its store has read it.
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                if (stored)
+                    store_2d(&maps.out, y_ring + ys * kYBytes + quad * 4096, u * kUnitCols,
+                             static_cast<int>(m0) + quad * 32);
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                if (prev >= 0) bar_arrive(y_empty + 8 * prev);
+            }
+            prev = ys;
+            if (++ys == plan.y_slots) {
+                ys = 0;
+                yph ^= 1;
+            }
+        }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
+    __syncthreads();
+    if (warp == 1) {
+        if (lane == 0) bar_drain(drain, 0, timer_ns() + kTimeoutNs);  // every MMA has completed
+        __syncwarp();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(kAccs * kUnitCols)
+                     : "memory");
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+// [rows, cols] bf16 with `stride` elements from row to row, boxes of 64
+// columns (128 bytes, swizzled) x box_rows rows.
+bool encode_map(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, int64_t stride,
+                uint32_t box_rows) {
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (enc == nullptr) return false;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
+    cuuint32_t box[2] = {64, box_rows};
+    cuuint32_t one[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box,
+               one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kSms = 148;
+
+int64_t row_tiles(int64_t rows) { return (rows + kTileRows - 1) / kTileRows; }
+
+// K splits of the shrink: enough items for two per SM, none below 8 blocks of
+// 64 (two rings' worth).
+int shrink_splits(int64_t rows, int64_t k) {
+    const int64_t want = 2 * kSms / row_tiles(rows), most = (k + 63) / 64 / 8;
+    int64_t s = want < most ? want : most;
+    if (s > 16) s = 16;
+    return s < 1 ? 1 : static_cast<int>(s);
+}
+
+// Column ranges of the expand: enough CTAs for two per SM.
+int expand_ranges(int64_t rows, int64_t n) {
+    const int64_t want = (2 * kSms + row_tiles(rows) - 1) / row_tiles(rows);
+    const int64_t most = (n + kUnitCols - 1) / kUnitCols;
+    return static_cast<int>(want < most ? want : most);
+}
+
+template <class K>
+cudaError_t allow_smem(K kernel, uint32_t bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(bytes));
+}
+
+template <int NB>
+cudaError_t launch_shrink(const ShrinkMaps &maps, const nvfp4_lora_args &p, int splits, float *partial,
+                          int *err, cudaStream_t stream) {
+    using Cfg = ShrinkConfig<NB>;
+    cudaError_t e = allow_smem(lora_shrink_kernel<NB>, Cfg::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    lora_shrink_kernel<NB><<<static_cast<unsigned>(row_tiles(p.rows) * splits), kThreads, Cfg::SMEM_BYTES,
+                             stream>>>(maps, p, splits, partial, err);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t lora_tile_workspace_bytes(int64_t rows, int64_t k, int64_t rank) {
+    return static_cast<size_t>(shrink_splits(rows, k)) * static_cast<size_t>(rows) *
+           static_cast<size_t>(rank) * sizeof(float);
+}
+
+cudaError_t launch_lora_tile(const nvfp4_lora_args &p, cudaStream_t stream) {
+    int *err = device_error_word();
+    if (err == nullptr) return cudaErrorUnknown;
+    ShrinkMaps sm;
+    ExpandMaps em;
+    std::memset(&sm, 0, sizeof(sm));
+    std::memset(&em, 0, sizeof(em));
+    if (!encode_map(&sm.x, p.x, p.k, p.rows, p.x_stride, kTileRows) ||
+        !encode_map(&sm.a, p.a, p.k, p.slots * p.rank, p.k, static_cast<uint32_t>(p.rank)) ||
+        !encode_map(&em.y, p.y, p.n, p.rows, p.y_stride, kTileRows) ||
+        !encode_map(&em.b, p.b, p.rank, p.slots * p.n, p.rank, kUnitCols) ||
+        !encode_map(&em.out, p.out, p.n, p.rows, p.out_stride, 32))
+        return cudaErrorInvalidValue;
+    const int splits = shrink_splits(p.rows, p.k);
+    float *partial = static_cast<float *>(p.workspace);
+    cudaError_t e = p.rank <= 64 ? launch_shrink<64>(sm, p, splits, partial, err, stream)
+                                 : launch_shrink<128>(sm, p, splits, partial, err, stream);
+    if (e != cudaSuccess) return e;
+    const ExpandPlan plan = expand_plan(p.rank);
+    e = allow_smem(lora_expand_kernel, plan.smem_bytes);
+    if (e != cudaSuccess) return e;
+    const int ranges = expand_ranges(p.rows, p.n);
+    lora_expand_kernel<<<static_cast<unsigned>(row_tiles(p.rows) * ranges), kThreads, plan.smem_bytes,
+                         stream>>>(em, p, plan, splits, ranges, partial, err);
+    return cudaGetLastError();
+}
+
+}  // namespace nvfp4
