@@ -303,8 +303,8 @@ typedef enum {
  *   row_group        device, rows int32, the request of each row, or NULL:
  *                    then rows / groups consecutive rows each (rows must be
  *                    a multiple of groups).  A row whose request is not in
- *                    [0, groups) is padding: it is not read, and its h, out,
- *                    q, block scales, s_dec and amax stay as they were.
+ *                    [0, groups) is padding: its h, out, q, block scales,
+ *                    s_dec and amax stay as they were.
  *   q, sf, s_dec_rows, amax_rows  the per-row NVFP4 quantization of out, bit
  *                    for bit as nvfp4_quantize_rowwise gives it for the bf16
  *                    out (amax_rows may be NULL); out itself may be NULL

@@ -25,6 +25,7 @@
 #include <cstdint>
 
 #include "block_ops.h"
+#include "gemm.h"
 #include "nvfp4_math.cuh"
 
 namespace nvfp4 {
@@ -143,6 +144,73 @@ __device__ __forceinline__ void norm_row(float (&x)[V][8], int kind, float eps, 
             for (int j = 0; j < 8; ++j) x[i][j] += b[j];
         }
     }
+}
+
+// Codes and block scale of vector `vec` of row r (eight bf16 values `o` whose
+// largest magnitude has the bits mx): lanes 2j and 2j + 1 hold a block of 16,
+// eight lanes a 4-byte word of block scales.  All lanes of a warp call;
+// vectors past the row are zero, so the padding blocks of its last word get
+// zero scales.
+__device__ __forceinline__ void quantize_vec(const nvfp4_residual_norm_args &a, int64_t r, int vec,
+                                             int nvec, uint4 o, uint32_t mx, float s_enc) {
+    const uint32_t mb = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+    const BlockScale bs = block_scale_direct(__uint_as_float(mb << 16), s_enc);
+    if (vec < nvec)
+        *reinterpret_cast<uint32_t *>(a.q + r * (a.cols >> 1) + vec * 4) = quantize_bf16x8(o, bs.inv);
+    const uint32_t sfc = vec < nvec ? bs.sf : 0u;
+    const uint32_t s1 = __shfl_down_sync(0xFFFFFFFFu, sfc, 2);
+    const uint32_t s2 = __shfl_down_sync(0xFFFFFFFFu, sfc, 4);
+    const uint32_t s3 = __shfl_down_sync(0xFFFFFFFFu, sfc, 6);
+    if ((vec & 7) == 0 && vec < nvec)
+        *reinterpret_cast<uint32_t *>(a.sf + sf_offset(r, int64_t(vec >> 1), (a.cols + 63) >> 6)) =
+            sfc | (s1 << 8) | (s2 << 16) | (s3 << 24);
+}
+
+// RN(a / 6) of a non-negative bf16 value in three fp32 operations.  Why it is
+// exact: c = RN(1/6) puts q = RN(a c) within two units of its last place of
+// a / 6, so a - 6 q is a small multiple of that unit and the fma gives it
+// without rounding; adding its sixth, computed to 24 bits, makes the value that
+// is rounded at the end agree with a / 6 to 2^-22 units, and a / 6 of a bf16 a
+// is 0, 1/3 or 2/3 of a unit above a representable number, at least 1/6 from
+// where rounding changes.  Values whose quotient could be subnormal take the
+// double product of nvfp4_math.cuh.
+__device__ __forceinline__ float sixth(float a) {
+    if (a < 7.888609e-31f /* 2^-100 */) return div6_short(a);
+    const float c = 1.0f / 6.0f;
+    const float q = __fmul_rn(a, c);
+    return __fmaf_rn(__fmaf_rn(-6.0f, q, a), c, q);
+}
+
+// Codes and block scales of two vectors of a thread, as quantize_vec gives them
+// for each.  The two lanes that share a block share its scale: the even one
+// computes the first vector's, the odd one the second's, one division each.
+__device__ __forceinline__ void quantize_two(const nvfp4_residual_norm_args &a, int64_t r, int vec0,
+                                             int vec1, bool second, uint4 o0, uint4 o1, uint32_t m0,
+                                             uint32_t m1, float s_enc) {
+    const bool odd = threadIdx.x & 1;
+    m0 = max(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, 1));
+    m1 = max(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, 1));
+    const uint32_t sf = e4m3_encode(__fmul_rn(sixth(__uint_as_float((odd ? m1 : m0) << 16)), s_enc));
+    const float value = e4m3_decode(sf);
+    float inv = 0.0f;
+    if (value != 0.0f) {
+        inv = __fdiv_rn(s_enc, value);
+        if (!isfinite(inv)) inv = FLT_MAX;
+    }
+    const float other = __shfl_xor_sync(0xFFFFFFFFu, inv, 1);
+    uint8_t *q = a.q + r * (a.cols >> 1);
+    *reinterpret_cast<uint32_t *>(q + vec0 * 4) = quantize_bf16x8(o0, odd ? other : inv);
+    if (second) *reinterpret_cast<uint32_t *>(q + vec1 * 4) = quantize_bf16x8(o1, odd ? inv : other);
+    // Four blocks (eight lanes) a word: lane 0 of the eight gathers the first
+    // vector's, lane 1 the second's.
+    const uint32_t s = odd && !second ? 0u : sf;
+    const uint32_t s1 = __shfl_down_sync(0xFFFFFFFFu, s, 2);
+    const uint32_t s2 = __shfl_down_sync(0xFFFFFFFFu, s, 4);
+    const uint32_t s3 = __shfl_down_sync(0xFFFFFFFFu, s, 6);
+    const int vec = odd ? vec1 - 1 : vec0;
+    if ((threadIdx.x & 6) == 0 && (!odd || second))
+        *reinterpret_cast<uint32_t *>(a.sf + sf_offset(r, int64_t(vec >> 1), (a.cols + 63) >> 6)) =
+            s | (s1 << 8) | (s2 << 16) | (s3 << 24);
 }
 
 // T threads per row, V vectors of 8 elements per thread (vector i of thread t
@@ -275,9 +343,6 @@ __global__ void __launch_bounds__(T *ROWS) residual_norm_kernel(const nvfp4_resi
     }
     if (a.q == nullptr) return;
 
-    // Per-row quantization: lanes 2j and 2j + 1 hold a block of 16, eight
-    // lanes a 4-byte word of block scales.  Vectors past the row are zero, so
-    // the padding blocks of its last word get zero scales.
     const float amax = rr.max(__uint_as_float(m << 16));
     const float s_enc = tensor_encode_scale(amax);
     if (tx == 0) {
@@ -285,20 +350,376 @@ __global__ void __launch_bounds__(T *ROWS) residual_norm_kernel(const nvfp4_resi
         if (a.amax_rows != nullptr) a.amax_rows[r] = amax;
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int vec = i * T + tx;
-        const uint32_t mb = max(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], 1));
-        const BlockScale bs = block_scale_direct(__uint_as_float(mb << 16), s_enc);
-        if (vec < nvec)
-            *reinterpret_cast<uint32_t *>(a.q + r * (a.cols >> 1) + vec * 4) =
-                quantize_bf16x8(o[i], bs.inv);
-        const uint32_t sfc = vec < nvec ? bs.sf : 0u;
-        const uint32_t s1 = __shfl_down_sync(0xFFFFFFFFu, sfc, 2);
-        const uint32_t s2 = __shfl_down_sync(0xFFFFFFFFu, sfc, 4);
-        const uint32_t s3 = __shfl_down_sync(0xFFFFFFFFu, sfc, 6);
-        if ((tx & 7) == 0 && vec < nvec)
-            *reinterpret_cast<uint32_t *>(a.sf + sf_offset(r, int64_t(vec >> 1), kb4)) =
-                sfc | (s1 << 8) | (s2 << 16) | (s3 << 24);
+    for (int i = 0; i < V; ++i) quantize_vec(a, r, i * T + tx, nvec, o[i], mx[i], s_enc);
+}
+
+// ---------------------------------------------------------------- many rows
+
+constexpr int kMaxStages = 8;
+constexpr int kRingBytes = 160 * 1024;
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr int kTimeoutTag = 48;
+
+__device__ __forceinline__ uint32_t s32(const void *p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+__device__ __forceinline__ uint64_t timer_ns() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// Waits for a row's copies.  A wait that gives up records it and goes on with
+// whatever the slot holds, as do all later ones at once: the threads of the
+// CTA stay together, and the call ends with the error word set.
+__device__ __forceinline__ void row_wait(uint32_t bar, uint32_t parity, volatile int *abort, int *err) {
+    if (bar_try(bar, parity)) return;
+    const uint64_t t0 = timer_ns();
+    while (!bar_try(bar, parity)) {
+        if (*abort) return;
+        if (timer_ns() - t0 > kTimeoutNs) {
+            if (atomicCAS(&err[0], 0, NVFP4_ERR_TIMEOUT) == 0) err[1] = kTimeoutTag;
+            *abort = 1;
+            return;
+        }
+    }
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            dst),
+        "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ uint4 lds_16B(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ void unpack4(uint4 v, float2 (&f)[4]) {
+    f[0] = make_float2(bf16_lo(v.x), bf16_hi(v.x));
+    f[1] = make_float2(bf16_lo(v.y), bf16_hi(v.y));
+    f[2] = make_float2(bf16_lo(v.z), bf16_hi(v.z));
+    f[3] = make_float2(bf16_lo(v.w), bf16_hi(v.w));
+}
+
+__device__ __forceinline__ uint4 pack4(const float2 (&f)[4]) {
+    return make_uint4(pack2(f[0].x, f[0].y), pack2(f[1].x, f[1].y), pack2(f[2].x, f[2].y),
+                      pack2(f[3].x, f[3].y));
+}
+
+// A weight or modulation vector's eight elements at `vec`, as loaded and as
+// four pairs.  `p` may be NULL (then `f` is not touched).
+template <bool kF32>
+struct RawVec {
+    uint4 w[kF32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void *p, int vec) {
+        if (p == nullptr) return;
+        const uint4 *q = static_cast<const uint4 *>(p) + vec * (kF32 ? 2 : 1);
+        w[0] = __ldg(q);
+        if (kF32) w[kF32 ? 1 : 0] = __ldg(q + 1);
+    }
+    __device__ __forceinline__ void get(float2 (&f)[4]) const {
+        if (kF32) {
+            const uint4 b = w[kF32 ? 1 : 0];
+            f[0] = make_float2(__uint_as_float(w[0].x), __uint_as_float(w[0].y));
+            f[1] = make_float2(__uint_as_float(w[0].z), __uint_as_float(w[0].w));
+            f[2] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y));
+            f[3] = make_float2(__uint_as_float(b.z), __uint_as_float(b.w));
+        } else {
+            unpack4(w[0], f);
+        }
+    }
+};
+
+constexpr int kVecs = 2;  // vectors of 8 columns per thread
+
+// Persistent CTAs of T = blockDim.x threads, two vectors per thread, rows
+// blockIdx.x, + gridDim.x, ...  y and the residual arrive by bulk copies,
+// `stages` rows ahead of the arithmetic, so the bytes in flight depend neither
+// on occupancy nor on a row's reductions.  What is left to keep small is the
+// instruction count: a row's fixed cost (barriers, reductions, addresses) is
+// shared by 32 columns per thread, and the arithmetic takes fp32 pairs.
+template <bool kFull, bool kQuant, bool kStreamF32, bool kVecF32>
+__global__ void __launch_bounds__(512, 2)
+    residual_norm_rows_kernel(const nvfp4_residual_norm_args a, const int64_t rows_per_group,
+                              const int stages, int *err) {
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ __align__(8) uint64_t bars[kMaxStages];
+    __shared__ __align__(16) float red[2][16];
+    __shared__ int abort_flag;
+    constexpr int V = kVecs;
+    const int T = blockDim.x, tx = threadIdx.x, lane = tx & 31, warp = tx >> 5;
+    const int nvec = static_cast<int>(a.cols) >> 3;
+    const bool second = kFull || T + tx < nvec;  // the first vector is always in the row
+    const float inv_cols = 1.0f / static_cast<float>(a.cols);
+    const uint32_t y_bytes = a.y != nullptr ? static_cast<uint32_t>(a.cols) * 2 : 0;
+    const uint32_t slot_bytes = y_bytes + static_cast<uint32_t>(a.cols) * (kStreamF32 ? 4 : 2);
+    const uint32_t ring_a = s32(ring), bar_a = s32(bars);
+    const size_t vec_size = kVecF32 ? 4 : 2;
+    if (tx == 0) {
+        for (int s = 0; s < stages; ++s)
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar_a + 8 * s));
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (tx < 32) red[tx >> 4][tx & 15] = 0.0f;  // the entries past the last warp stay 0
+    __syncthreads();
+
+    auto fetch = [&](int64_t r, int slot) __attribute__((always_inline)) {
+        const uint32_t bar = bar_a + 8 * slot, dst = ring_a + slot * slot_bytes;
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(slot_bytes)
+                     : "memory");
+        if (y_bytes) bulk_load(dst, static_cast<const uint16_t *>(a.y) + r * a.y_stride, y_bytes, bar);
+        bulk_load(dst + y_bytes,
+                  static_cast<const uint8_t *>(a.residual) + r * a.residual_stride * (kStreamF32 ? 4 : 2),
+                  slot_bytes - y_bytes, bar);
+    };
+    int turn = 0;
+    auto reduce = [&](float v, auto op) __attribute__((always_inline)) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+        if (lane == 0) red[turn][warp] = v;
+        __syncthreads();
+        const float4 *b = reinterpret_cast<const float4 *>(red[turn]);
+        turn ^= 1;
+        v = op(op(b[0].x, b[0].y), op(b[0].z, b[0].w));
+        for (int w = 4; w < T >> 5; w += 4) v = op(v, op(op(b[w >> 2].x, b[w >> 2].y), op(b[w >> 2].z, b[w >> 2].w)));
+        return v;
+    };
+    auto add = [](float u, float v) __attribute__((always_inline)) { return u + v; };
+    auto larger = [](float u, float v) __attribute__((always_inline)) {
+        return __uint_as_float(::max(__float_as_uint(u), __float_as_uint(v)));
+    };
+    // x <- x - mean for a layer norm; returns 1 / sqrt(mean(x^2) + eps).
+    auto centred_inverse = [&](float2 (&x)[V][4], int kind, float eps) __attribute__((always_inline)) {
+        if (kind == NVFP4_NORM_LAYER) {
+            float2 s = both(0.0f);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s = __fadd2_rn(s, x[i][j]);
+            const float2 mean = both(-reduce(s.x + s.y, add) * inv_cols);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i == 0 || second) {  // the others stay zero
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[i][j] = __fadd2_rn(x[i][j], mean);
+                }
+        }
+        float2 s2 = both(0.0f);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s2 = __ffma2_rn(x[i][j], x[i][j], s2);
+        return rsqrtf(fmaf(reduce(s2.x + s2.y, add), inv_cols, eps));
+    };
+    auto group_of = [&](int64_t r) __attribute__((always_inline)) {
+        return a.row_group != nullptr ? int64_t(__ldg(a.row_group + r)) : r / rows_per_group;
+    };
+    // x <- x * vector (or x + vector) where there is one.
+    auto times = [&](float2 (&x)[V][4], const void *p) __attribute__((always_inline)) {
+        if (p == nullptr) return;
+        RawVec<kVecF32> raw[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i == 0 || second) raw[i].load(p, i * T + tx);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (i > 0 && !second) continue;
+            float2 f[4];
+            raw[i].get(f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[i][j] = __fmul2_rn(x[i][j], f[j]);
+        }
+    };
+    auto plus = [&](float2 (&x)[V][4], const void *p) __attribute__((always_inline)) {
+        if (p == nullptr) return;
+        RawVec<kVecF32> raw[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i == 0 || second) raw[i].load(p, i * T + tx);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (i > 0 && !second) continue;
+            float2 f[4];
+            raw[i].get(f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[i][j] = __fadd2_rn(x[i][j], f[j]);
+        }
+    };
+
+    const int64_t step = gridDim.x;
+    int64_t r = blockIdx.x, issued = 0;  // issued: rows asked for (thread 0)
+    if (tx == 0)
+        for (; issued < stages && r + issued * step < a.rows; ++issued)
+            fetch(r + issued * step, static_cast<int>(issued));
+    int64_t next = r < a.rows ? group_of(r) : -1;
+    int slot = 0;
+    uint32_t parity = 0;
+    // This thread's first vector of the current row of h and out.
+    uint8_t *hp = static_cast<uint8_t *>(a.h) + (r * a.h_stride + tx * 8) * (kStreamF32 ? 4 : 2);
+    uint8_t *op = static_cast<uint8_t *>(a.out) + (r * a.out_stride + tx * 8) * 2;
+    const int64_t h_step = step * a.h_stride * (kStreamF32 ? 4 : 2), o_step = step * a.out_stride * 2;
+    for (; r < a.rows; r += step, hp += h_step, op += o_step) {
+        const int64_t group = next;
+        if (r + step < a.rows) next = group_of(r + step);
+        const bool live = group >= 0 && group < a.groups;
+        row_wait(bar_a + 8 * slot, parity, &abort_flag, err);
+        const uint32_t ys = ring_a + slot * slot_bytes, rs = ys + y_bytes;
+        uint4 yv[V], rv[kStreamF32 ? 2 * V : V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int vec = i * T + tx;
+            if (!kFull && i > 0) {
+                yv[i] = rv[i] = make_uint4(0, 0, 0, 0);
+                if (kStreamF32) rv[(kStreamF32 ? V : 0) + i] = make_uint4(0, 0, 0, 0);
+            }
+            if (i == 0 || second) {
+                yv[i] = y_bytes ? lds_16B(ys + vec * 16) : make_uint4(0, 0, 0, 0);
+                if (kStreamF32) {
+                    rv[i] = lds_16B(rs + vec * 32);
+                    rv[(kStreamF32 ? V : 0) + i] = lds_16B(rs + vec * 32 + 16);
+                } else {
+                    rv[i] = lds_16B(rs + vec * 16);
+                }
+            }
+        }
+        // The slot is free once every thread has read it: at the row's first
+        // reduction, or here where none is sure to come.
+        if (!live || (a.post_norm == NVFP4_NORM_NONE && a.pre_norm == NVFP4_NORM_NONE)) __syncthreads();
+        if (live) {
+            float2 x[V][4];
+#pragma unroll
+            for (int i = 0; i < V; ++i) unpack4(yv[i], x[i]);
+            if (a.post_norm != NVFP4_NORM_NONE) {
+                const float2 inv = both(centred_inverse(x, a.post_norm, a.post_eps));
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[i][j] = __fmul2_rn(x[i][j], inv);
+                times(x, a.post_weight);
+                plus(x, a.post_bias);
+            }
+            const float2 rscale = both(a.residual_scale), bscale = both(a.branch_scale);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int vec = i * T + tx;
+                if (i > 0 && !second) continue;
+                float2 res[4], gf[4];
+                if (kStreamF32) {
+                    const uint4 lo = rv[i], hi = rv[(kStreamF32 ? V : 0) + i];
+                    res[0] = make_float2(__uint_as_float(lo.x), __uint_as_float(lo.y));
+                    res[1] = make_float2(__uint_as_float(lo.z), __uint_as_float(lo.w));
+                    res[2] = make_float2(__uint_as_float(hi.x), __uint_as_float(hi.y));
+                    res[3] = make_float2(__uint_as_float(hi.z), __uint_as_float(hi.w));
+                } else {
+                    unpack4(rv[i], res);
+                }
+                if (a.gate != nullptr) {
+                    RawVec<kVecF32> gate;
+                    gate.load(static_cast<const uint8_t *>(a.gate) + group * a.gate_stride * vec_size, vec);
+                    gate.get(gf);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[i][j] = __fmul2_rn(x[i][j], gf[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    x[i][j] = __ffma2_rn(rscale, res[j], __fmul2_rn(bscale, x[i][j]));
+                if (a.h != nullptr) {
+                    if (kStreamF32) {
+                        float4 *o = reinterpret_cast<float4 *>(hp + i * T * 32);
+                        o[0] = make_float4(x[i][0].x, x[i][0].y, x[i][1].x, x[i][1].y);
+                        o[1] = make_float4(x[i][2].x, x[i][2].y, x[i][3].x, x[i][3].y);
+                    } else {
+                        *reinterpret_cast<uint4 *>(hp + i * T * 16) = pack4(x[i]);
+                    }
+                }
+            }
+            if (a.pre_norm != NVFP4_NORM_NONE) {
+                const float2 inv = both(centred_inverse(x, a.pre_norm, a.pre_eps));
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[i][j] = __fmul2_rn(x[i][j], inv);
+                times(x, a.pre_weight);
+                plus(x, a.pre_bias);
+                if (a.scale != nullptr) {
+                    const uint8_t *sp = static_cast<const uint8_t *>(a.scale) + group * a.scale_stride * vec_size;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        if (i > 0 && !second) continue;
+                        RawVec<kVecF32> raw;
+                        float2 f[4];
+                        raw.load(sp, i * T + tx);
+                        raw.get(f);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) x[i][j] = __ffma2_rn(x[i][j], f[j], x[i][j]);
+                    }
+                }
+                if (a.shift != nullptr)
+                    plus(x, static_cast<const uint8_t *>(a.shift) + group * a.shift_stride * vec_size);
+                uint4 o[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int vec = i * T + tx;
+                    o[i] = pack4(x[i]);  // zero past the row
+                    if (a.out != nullptr && (i == 0 || second))
+                        *reinterpret_cast<uint4 *>(op + i * T * 16) = o[i];
+                }
+                if (kQuant) {
+                    const uint32_t m0 = absmax_bf16x8(o[0]), m1 = absmax_bf16x8(o[1]);
+                    const float amax = reduce(__uint_as_float(::max(m0, m1) << 16), larger);
+                    const float s_enc = tensor_encode_scale(amax);
+                    if (tx == 0) {
+                        a.s_dec_rows[r] = __fdiv_rn(1.0f, s_enc);
+                        if (a.amax_rows != nullptr) a.amax_rows[r] = amax;
+                    }
+                    quantize_two(a, r, tx, T + tx, second, o[0], o[1], m0, m1, s_enc);
+                }
+            }
+        }
+        if (tx == 0 && r + stages * step < a.rows && !*static_cast<volatile int *>(&abort_flag)) {
+            fetch(r + stages * step, slot);
+            ++issued;
+        }
+        if (++slot == stages) {
+            slot = 0;
+            parity ^= 1;
+        }
+    }
+    if (tx == 0 && *static_cast<volatile int *>(&abort_flag)) {  // copies still in flight
+        const uint64_t deadline = timer_ns() + kTimeoutNs;
+        for (int64_t k = issued > stages ? issued - stages : 0; k < issued; ++k)
+            while (!bar_try(bar_a + 8 * static_cast<int>(k % stages), (k / stages) & 1))
+                if (timer_ns() > deadline) break;
+    }
+    if (kQuant) {  // padding rows of the tiled scales
+        const int64_t rows_pad = (a.rows + 127) & ~int64_t(127), kb4 = (a.cols + 63) >> 6;
+        for (int64_t z = a.rows + blockIdx.x; z < rows_pad; z += step)
+            for (int64_t c = tx; c < kb4; c += T)
+                *reinterpret_cast<uint32_t *>(a.sf + sf_offset(z, 4 * c, kb4)) = 0u;
     }
 }
 
@@ -314,26 +735,60 @@ cudaError_t launch(const nvfp4_residual_norm_args &a, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
+template <bool kFull, bool kQuant, bool kStreamF32, bool kVecF32>
+cudaError_t launch_rows_as(const nvfp4_residual_norm_args &a, int num_sms, cudaStream_t stream) {
+    auto *kernel = residual_norm_rows_kernel<kFull, kQuant, kStreamF32, kVecF32>;
+    int *err = device_error_word();
+    if (err == nullptr) return cudaErrorUnknown;
+    const int threads = static_cast<int>((a.cols / 8 + kVecs - 1) / kVecs + 31) / 32 * 32;
+    const int64_t slot = a.cols * ((a.y != nullptr ? 2 : 0) + (kStreamF32 ? 4 : 2));
+    // 1024 threads per SM by registers, in at most 16 CTAs; kRingBytes of rows
+    // in flight between them.
+    int per_sm = 1024 / threads;
+    if (per_sm > 16) per_sm = 16;
+    int64_t stages = kRingBytes / per_sm / slot;
+    stages = stages < 2 ? 2 : stages > kMaxStages ? kMaxStages : stages;
+    const int smem = static_cast<int>(stages * slot);
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int64_t grid = static_cast<int64_t>(num_sms) * per_sm;
+    kernel<<<static_cast<unsigned>(grid < a.rows ? grid : a.rows), threads, smem, stream>>>(
+        a, (a.rows + a.groups - 1) / a.groups, static_cast<int>(stages), err);
+    return cudaGetLastError();
+}
+
+template <bool kFull, bool kQuant>
+cudaError_t launch_rows_of(const nvfp4_residual_norm_args &a, int num_sms, cudaStream_t stream) {
+    const bool v32 = a.vector_dtype == NVFP4_F32;
+    if (a.stream_dtype == NVFP4_F32)
+        return v32 ? launch_rows_as<kFull, kQuant, true, true>(a, num_sms, stream)
+                   : launch_rows_as<kFull, kQuant, true, false>(a, num_sms, stream);
+    return v32 ? launch_rows_as<kFull, kQuant, false, true>(a, num_sms, stream)
+               : launch_rows_as<kFull, kQuant, false, false>(a, num_sms, stream);
+}
+
+cudaError_t launch_rows(const nvfp4_residual_norm_args &a, int num_sms, cudaStream_t stream) {
+    // Whole warps of whole vectors need no bounds checks.
+    if (a.cols % (32 * 8 * kVecs) == 0)
+        return a.q != nullptr ? launch_rows_of<true, true>(a, num_sms, stream)
+                              : launch_rows_of<true, false>(a, num_sms, stream);
+    return a.q != nullptr ? launch_rows_of<false, true>(a, num_sms, stream)
+                          : launch_rows_of<false, false>(a, num_sms, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_residual_norm(const nvfp4_residual_norm_args &a, int num_sms,
                                  cudaStream_t stream) {
     const int64_t c = a.cols;
-    // Few rows: one vector per thread, the shortest chain.  Many: two or four,
-    // so that a row's reductions cost fewer threads.
-    const bool few = a.rows <= 2 * int64_t(num_sms);
+    if (a.rows > 2 * int64_t(num_sms) && c > 256 && c <= 8192) return launch_rows(a, num_sms, stream);
+    // Few rows: one vector per thread, the shortest chain.
     if (c <= 256) return launch<32, 1, 4>(a, stream);
-    if (few) {
-        if (c <= 1024) return launch<128, 1, 1>(a, stream);
-        if (c <= 2048) return launch<256, 1, 1>(a, stream);
-        if (c <= 4096) return launch<512, 1, 1>(a, stream);
-        if (c <= 8192) return launch<1024, 1, 1>(a, stream);
-    }
-    if (c <= 512) return launch<32, 2, 4>(a, stream);
-    if (c <= 1024) return launch<32, 4, 4>(a, stream);
-    if (c <= 2048) return launch<128, 2, 1>(a, stream);
-    if (c <= 4096) return launch<256, 2, 1>(a, stream);
-    if (c <= 8192) return launch<256, 4, 1>(a, stream);
+    if (c <= 1024) return launch<128, 1, 1>(a, stream);
+    if (c <= 2048) return launch<256, 1, 1>(a, stream);
+    if (c <= 4096) return launch<512, 1, 1>(a, stream);
+    if (c <= 8192) return launch<1024, 1, 1>(a, stream);
     if (c <= 16384) return launch<512, 4, 1>(a, stream);
     return launch<1024, 4, 1>(a, stream);
 }

@@ -88,15 +88,20 @@ def test_widths(nv, rows, cols):
 @pytest.mark.parametrize("vec", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("post", [None, "rms", "layer"])
 @pytest.mark.parametrize("pre", [None, "rms", "layer"])
-def test_types_and_norms(nv, stream, vec, post, pre):
-    for gate, mod, weights in ((False, False, True), (True, pre is not None, False)):
-        _check(nv, _case(37, 640, stream=stream, vec=vec, post=post, pre=pre, gate=gate, mod=mod,
+@pytest.mark.parametrize("rows,cols", [(37, 640), (1999, 1296), (700, 4112), (620, 5136)])
+def test_types_and_norms(nv, stream, vec, post, pre, rows, cols):
+    for gate, mod, weights in ((False, False, True), (True, pre is not None, False),
+                               (True, pre is not None, True)):
+        _check(nv, _case(rows, cols, stream=stream, vec=vec, post=post, pre=pre, gate=gate, mod=mod,
                          groups=5, weights=weights), residual_scale=0.75, branch_scale=-1.5)
+    code, tag = nv.device_error()
+    assert code == 0, f"device wait timed out (tag {tag})"
 
 
-def test_start_of_a_model(nv):
+@pytest.mark.parametrize("rows", [65, 650])
+def test_start_of_a_model(nv, rows):
     """No y: the norm of the (scaled) stream alone."""
-    residual, _, row_group, kw, ref = _case(65, 1536, pre="layer", mod=True, groups=2)
+    residual, _, row_group, kw, ref = _case(rows, 1536, pre="layer", mod=True, groups=2)
     r = nv.residual_norm(residual, row_group=row_group, residual_scale=3.0, **_norms(nv, kw))
     _, _, o, e_o = residual_norm64(residual, None, residual_scale=3.0, **ref)
     assert r.h is None
@@ -122,9 +127,10 @@ def test_consecutive_rows_without_row_group(nv):
         nv.residual_norm(residual[:59], y[:59], **_norms(nv, kw))
 
 
-def test_unsorted_requests_and_one_vector_for_all(nv):
-    residual, y, _, kw, ref = _case(90, 384, gate=True, mod=True, groups=6)
-    g = torch.randint(0, 6, (90,), generator=_gen(1), device="cuda")
+@pytest.mark.parametrize("rows", [90, 1700])
+def test_unsorted_requests_and_one_vector_for_all(nv, rows):
+    residual, y, _, kw, ref = _case(rows, 384, gate=True, mod=True, groups=6)
+    g = torch.randint(0, 6, (rows,), generator=_gen(1), device="cuda")
     kw["gate"] = ref["gate"] = kw["gate"][2]     # [cols]
     ref["group"] = g
     r = nv.residual_norm(residual, y, row_group=g.to(torch.int32), **_norms(nv, kw))
@@ -133,7 +139,7 @@ def test_unsorted_requests_and_one_vector_for_all(nv):
     assert_close(r.out, o, e_o)
 
 
-@pytest.mark.parametrize("rows,cols", [(5, 512), (129, 1040), (400, 4096)])
+@pytest.mark.parametrize("rows,cols", [(5, 512), (129, 1040), (400, 4096), (5000, 1040), (1000, 8192)])
 def test_padding_rows_stay_as_they_were(nv, rows, cols):
     residual, y, row_group, kw, ref = _case(rows, cols, pad=True, gate=True, mod=True, groups=3)
     live = (row_group >= 0) & (row_group < 3)
@@ -163,9 +169,9 @@ def test_padding_rows_stay_as_they_were(nv, rows, cols):
 
 
 @pytest.mark.parametrize("stream", [torch.bfloat16, torch.float32])
-def test_strided_and_in_place(nv, stream):
+@pytest.mark.parametrize("rows,cols", [(70, 528), (3000, 528), (900, 6160)])
+def test_strided_and_in_place(nv, stream, rows, cols):
     """Column slices of wider buffers, h over the residual, out over y."""
-    rows, cols = 70, 528
     residual, y, row_group, kw, ref = _case(rows, cols, stream=stream, post="layer", pre="rms", gate=True, mod=True)
     h, e_h, o, e_o = residual_norm64(residual, y, **ref)
     wide_r = torch.full((rows, cols + 64), 3.0, dtype=stream, device="cuda")
@@ -180,9 +186,10 @@ def test_strided_and_in_place(nv, stream):
     assert (wide_r[:, :32] == 3.0).all() and (wide_r[:, 32 + cols:] == 3.0).all() and (wide_y[:, :cols] == 4.0).all()
 
 
-def test_offsets_past_32_bits(nv):
+@pytest.mark.parametrize("rows,cols", [(270, 256), (310, 512)])
+def test_offsets_past_32_bits(nv, rows, cols):
     """Rows 2^23 elements apart: the last ones start beyond 2^31 elements."""
-    rows, cols, stride = 270, 256, 1 << 23
+    stride = 1 << 23
     residual, y, row_group, kw, ref = _case(rows, cols)
     far = torch.empty(rows * stride, dtype=torch.bfloat16, device="cuda").view(rows, stride)[:, :cols]
     far.copy_(y)
@@ -193,8 +200,9 @@ def test_offsets_past_32_bits(nv):
     assert_close(r.h, h, e_h)
 
 
-def test_rows_of_zeros_and_of_large_values(nv):
-    residual, y, row_group, kw, ref = _case(8, 1024, pre="layer", weights=False)
+@pytest.mark.parametrize("rows", [8, 400])
+def test_rows_of_zeros_and_of_large_values(nv, rows):
+    residual, y, row_group, kw, ref = _case(rows, 1024, pre="layer", weights=False)
     residual[0], y[0] = 0, 0                      # variance 0: out = 0
     residual[1], y[1] = 5.0, 0                    # constant row of a layer norm
     residual[2] *= 1e15
@@ -221,9 +229,10 @@ def test_oracle_codes(nv, orc):
     assert np.array_equal(r.quant.s_dec.cpu().numpy(), osd)
 
 
-def test_streams_and_graph(nv):
+@pytest.mark.parametrize("rows", [200, 800])
+def test_streams_and_graph(nv, rows):
     """Side stream with its inputs made there; a captured call replayed on new values."""
-    case = _case(200, 2048, post="rms", gate=True, mod=True, groups=2)
+    case = _case(rows, 2048, post="rms", gate=True, mod=True, groups=2)
     residual, y, row_group, kw, ref = case
     norms = _norms(nv, kw)
     side = torch.cuda.Stream()
