@@ -1,24 +1,25 @@
 // Low-rank adapters for many rows (the mathematics is stated in lora.cu): two
 // launches on 128-row tiles, both tcgen05 with TMA-fed shared memory.
 //
-// lora_shrink_kernel   partial[sp][m][:] = A[s] x[m] over the K range of split sp.
-//   Item = (row tile, split).  A stage is the tile's 128 x 64 piece of x and,
-//   side by side as one B operand, the matching rank x 64 pieces of up to
-//   G = NB / rank different adapters, so a tile whose rows belong to G requests
-//   still reads x once; each row's epilogue thread keeps its own adapter's
-//   columns.  x is split over K when the row tiles alone leave SMs idle; the
-//   partial sums are added in a fixed order by the next launch, so the
-//   result does not depend on timing.
-// lora_expand_kernel   out[m][n] = bf16(y[m][n] + B[s] t[m]),
-//   t[m] = scale[s] * sum_sp partial[sp][m].
+// lora_shrink_kernel   t[m] = scale[s] * A[s] x[m].
+//   A cluster of `splits` CTAs per row tile, each over its share of K.  A stage
+//   is the tile's 128 x 64 piece of x and, side by side as one B operand, the
+//   matching rank x 64 pieces of up to G = NB / rank different adapters, so a
+//   tile whose rows belong to G requests still reads x once; each row's
+//   epilogue thread keeps its own adapter's columns.  The splits' fp32 sums meet
+//   in the workspace: after a cluster barrier each CTA adds up its share of the
+//   rows, in the order of the splits, so the result does not depend on timing.
+//   t is written as the sum of two bf16 (hi + lo, 16 mantissa bits), as the
+//   expand's MMA takes it.
+// lora_expand_kernel   out[m][n] = bf16(y[m][n] + B[s] t[m]).
 //   A CTA keeps t of its row tile in shared memory and walks over units of 64
 //   columns: y by TMA into a ring, B's 64 x rank piece by TMA, the product in
-//   tensor memory, added to y in place in the ring, out by TMA.  t is kept as
-//   the sum of two bf16 (hi + lo, 16 mantissa bits), two MMAs per 16 ranks, so
-//   the product keeps nearly fp32 accuracy while B, which is bf16 already,
-//   needs no second copy.  A tile with rows of several adapters makes one
-//   product per adapter, each row taking its own adapter's: nothing of another
-//   adapter, not even NaN, reaches a row.
+//   tensor memory (two MMAs per 16 ranks, for hi and lo, so that it keeps nearly
+//   fp32 accuracy while B, which is bf16 already, needs no second copy), added
+//   to y in place in the ring, out by TMA.  A tile with rows of several adapters
+//   makes one product per adapter, each row taking its own adapter's: nothing of
+//   another adapter, not even NaN, reaches a row.  The launch overlaps the
+//   shrink's (programmatic dependence): only t waits for it.
 //
 // What bounds them: HBM (x once; y and out once).  Rank 128 is 64 flops per byte
 // of x, above what the register-operand MMAs sustain beside the loads and far
@@ -188,6 +189,23 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&f)[16]) {
     for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(r[i]);
 }
 
+// 64 columns of this warp's 32 lanes, complete on return.
+__device__ __forceinline__ void tmem_ld64(uint32_t addr, uint32_t (&r)[64]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(addr)
+        : "memory");
+}
+
+// The pair of bf16 in w plus two fp32 values, rounded once.
+__device__ __forceinline__ uint32_t add_pair(uint32_t w, uint32_t lo, uint32_t hi) {
+    const __nv_bfloat162 o =
+        __floats2bfloat162_rn(bf16_lo(w) + __uint_as_float(lo), bf16_hi(w) + __uint_as_float(hi));
+    return *reinterpret_cast<const uint32_t *>(&o);
+}
+
 __device__ __forceinline__ uint4 ld_shared_16B(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -251,12 +269,40 @@ __device__ __forceinline__ void find_slots(TileSlots &ts, const nvfp4_lora_args 
     __syncthreads();
 }
 
+// How t is laid out for a rank: rows of 64-element (128-byte) groups, hi's
+// groups first, then lo's; up to rank 32 both share one group, lo from its
+// 32nd element on.
+struct TLayout {
+    int groups;     // 128-byte groups of a row
+    int lo_at;      // element where lo starts
+    __host__ __device__ explicit TLayout(int rank)
+        : groups(rank <= 32 ? 1 : rank <= 64 ? 2 : 4), lo_at(rank <= 32 ? 32 : groups * 32) {}
+};
+
+// Eight values of t as hi and lo, 16 bytes each.
+__device__ __forceinline__ void store_t8(const float *t, uint16_t *hi_dst, uint16_t *lo_dst) {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(t[2 * j], t[2 * j + 1]);
+        const float2 back = __bfloat1622float2(h);
+        // An infinite (or NaN) value is carried by hi alone.
+        const float l0 = isfinite(back.x) ? t[2 * j] - back.x : 0.0f;
+        const float l1 = isfinite(back.y) ? t[2 * j + 1] - back.y : 0.0f;
+        const __nv_bfloat162 l = __floats2bfloat162_rn(l0, l1);
+        hi[j] = *reinterpret_cast<const uint32_t *>(&h);
+        lo[j] = *reinterpret_cast<const uint32_t *>(&l);
+    }
+    *reinterpret_cast<uint4 *>(hi_dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4 *>(lo_dst) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+}
+
 struct alignas(64) ShrinkMaps {
     CUtensorMap x, a;
 };
 
 struct alignas(64) ExpandMaps {
-    CUtensorMap y, b, out;
+    CUtensorMap y, b, out, t;
 };
 
 // ---------------------------------------------------------------- shrink
@@ -272,7 +318,7 @@ struct ShrinkConfig {
 template <int NB>
 __global__ void __launch_bounds__(kThreads)
     lora_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const nvfp4_lora_args p,
-                       const int splits, float *__restrict__ partial, int *err) {
+                       const int splits, float *partial, uint16_t *t, int *err) {
     using Cfg = ShrinkConfig<NB>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ TileSlots ts;
@@ -304,8 +350,9 @@ __global__ void __launch_bounds__(kThreads)
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     find_slots(ts, p, m0);
-    if (ts.count == 0) return;  // no row has an adapter
+    if (ts.count == 0) return;  // no row has an adapter (the same in the whole cluster)
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          s32(&tmem_holder)),
@@ -395,7 +442,10 @@ __global__ void __launch_bounds__(kThreads)
     } else {
         const int quad = warp & 3, row = quad * 32 + lane;
         const int mine = ts.row[row];
+        const TLayout tl(rank);
         float *dst = partial + (int64_t(split) * p.rows + m0 + row) * rank;
+        uint16_t *tdst = t + (m0 + row) * (tl.groups * 64);
+        const float c = mine >= 0 ? __ldg(p.scale + ts.list[mine]) : 0.0f;
         for (int q = 0; q < passes; ++q) {
             const int d0 = q * group, d1 = min(ts.count, d0 + group);
             if (!bar_wait_warp(acc_full + 8 * (q & 1), (q >> 1) & 1, ab, 43)) break;
@@ -406,7 +456,13 @@ __global__ void __launch_bounds__(kThreads)
                     float f[16];
                     __syncwarp();
                     tmem_ld16(acc + (d - d0) * rank + r, f);
-                    if (mine == d) {  // also false for rows past the last one
+                    if (mine != d) continue;  // also rows past the last one
+                    if (splits == 1) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) f[j] *= c;
+                        store_t8(f, tdst + r, tdst + tl.lo_at + r);
+                        store_t8(f + 8, tdst + r + 8, tdst + tl.lo_at + r + 8);
+                    } else {
                         float4 *o = reinterpret_cast<float4 *>(dst + r);
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
@@ -426,6 +482,33 @@ __global__ void __launch_bounds__(kThreads)
                      "r"(Cfg::TMEM_COLS)
                      : "memory");
     }
+    if (splits == 1) return;
+    // Every split's sums are written: this CTA's share of the rows, eight ranks
+    // per thread at a time, in the order of the splits.
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                     : "memory");
+    const TLayout tl(rank);
+    const int eights = rank >> 3, share = kTileRows / splits;
+    for (int i = threadIdx.x; i < share * eights; i += kThreads) {
+        const int row = split * share + i / eights, r = (i % eights) * 8;
+        const int d = ts.row[row];
+        if (d < 0) continue;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+        const float *src = partial + (m0 + row) * rank + r;
+        for (int s = 0; s < splits; ++s, src += p.rows * rank) {
+            const float4 a = *reinterpret_cast<const float4 *>(src);
+            const float4 b = *reinterpret_cast<const float4 *>(src + 4);
+            v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+            v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+        }
+        const float c = __ldg(p.scale + ts.list[d]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= c;
+        uint16_t *o = t + (m0 + row) * (tl.groups * 64) + r;
+        store_t8(v, o, o + tl.lo_at);
+    }
 }
 
 // ---------------------------------------------------------------- expand
@@ -434,7 +517,7 @@ __global__ void __launch_bounds__(kThreads)
 struct ExpandPlan {
     int y_slots, b_slots;     // ring depths
     uint32_t b_bytes;         // one B piece: 64 rows x (64 ranks x chunks)
-    uint32_t lo_offset;       // from t's hi part to its lo part
+    uint32_t lo_offset;       // bytes from t's hi part to its lo part
     uint32_t t_bytes;
     int chunks;               // 64-rank chunks
     uint32_t smem_bytes;
@@ -460,11 +543,10 @@ ExpandPlan expand_plan(int64_t rank) {
 
 __global__ void __launch_bounds__(kThreads)
     lora_expand_kernel(const __grid_constant__ ExpandMaps maps, const nvfp4_lora_args p,
-                       const ExpandPlan plan, const int splits, const int ranges,
-                       const float *__restrict__ partial, int *err) {
+                       const ExpandPlan plan, const int ranges, int *err) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ TileSlots ts;
-    __shared__ __align__(8) uint64_t bars[2 * kMaxYSlots + 2 * kMaxBSlots + 2 * kAccs + 1];
+    __shared__ __align__(8) uint64_t bars[2 * kMaxYSlots + 2 * kMaxBSlots + 2 * kAccs + 2];
     __shared__ uint32_t tmem_holder;
     __shared__ int abort_flag;
     const uint32_t t_base = (s32(smem_raw) + 1023u) & ~1023u;
@@ -472,7 +554,7 @@ __global__ void __launch_bounds__(kThreads)
     const uint32_t y_full = s32(bars), y_empty = y_full + 8 * kMaxYSlots;
     const uint32_t b_full = y_empty + 8 * kMaxYSlots, b_empty = b_full + 8 * kMaxBSlots;
     const uint32_t d_full = b_empty + 8 * kMaxBSlots, d_empty = d_full + 8 * kAccs;
-    const uint32_t drain = d_empty + 8 * kAccs;
+    const uint32_t t_full = d_empty + 8 * kAccs, drain = t_full + 8;
     const Abort ab{&abort_flag, err};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tile = blockIdx.x / ranges, range = blockIdx.x % ranges;
@@ -495,61 +577,22 @@ __global__ void __launch_bounds__(kThreads)
             bar_init(d_full + 8 * s, 1);
             bar_init(d_empty + 8 * s, 4);
         }
+        bar_init(t_full, 1);
         bar_init(drain, 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     find_slots(ts, p, m0);
-    if (ts.count == 0 && p.out == p.y) return;  // nothing to add and nothing to copy
+    if (ts.count == 0 && p.out == p.y) {  // nothing to add and nothing to copy
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          s32(&tmem_holder)),
                      "r"(kAccs * kUnitCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
-    // t of the tile's rows: eight ranks per thread at a time.
-    if (ts.count > 0) {
-        const int groups = rank >> 3;
-        for (int i = threadIdx.x; i < kTileRows * groups; i += kThreads) {
-            const int row = i / groups, r = (i % groups) * 8;
-            float t[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) t[j] = 0.0f;
-            const int d = ts.row[row];
-            if (d >= 0) {
-                const float *src = partial + (m0 + row) * rank + r;
-                for (int s = 0; s < splits; ++s, src += p.rows * rank) {
-                    const float4 a = *reinterpret_cast<const float4 *>(src);
-                    const float4 b = *reinterpret_cast<const float4 *>(src + 4);
-                    t[0] += a.x; t[1] += a.y; t[2] += a.z; t[3] += a.w;
-                    t[4] += b.x; t[5] += b.y; t[6] += b.z; t[7] += b.w;
-                }
-                const float c = __ldg(p.scale + ts.list[d]);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) t[j] *= c;
-            }
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(t[2 * j], t[2 * j + 1]);
-                const float2 back = __bfloat1622float2(h);
-                // An infinite (or NaN) value is carried by hi alone.
-                const float l0 = isfinite(back.x) ? t[2 * j] - back.x : 0.0f;
-                const float l1 = isfinite(back.y) ? t[2 * j + 1] - back.y : 0.0f;
-                const __nv_bfloat162 l = __floats2bfloat162_rn(l0, l1);
-                hi[j] = *reinterpret_cast<const uint32_t *>(&h);
-                lo[j] = *reinterpret_cast<const uint32_t *>(&l);
-            }
-            const uint32_t at = t_base + (r >> 6) * (kTileRows * 128) + row * 128;
-            const uint32_t col = (r & 63) * 2;  // bytes in the 128-byte row
-            const uint32_t lo_col = plan.lo_offset == 64 ? col + 64 : col;
-            const uint32_t lo_at = plan.lo_offset == 64 ? at : at + plan.lo_offset;
-            const uint32_t swz = (row & 7) << 4;
-            st_shared_16B(at + (col ^ swz), make_uint4(hi[0], hi[1], hi[2], hi[3]));
-            st_shared_16B(lo_at + (lo_col ^ swz), make_uint4(lo[0], lo[1], lo[2], lo[3]));
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     fence_before();
     __syncthreads();
@@ -575,6 +618,13 @@ __global__ void __launch_bounds__(kThreads)
                     ys = 0;
                     yph ^= 1;
                 }
+                if (u == u0 && count > 0) {  // the shrink's result
+                    asm volatile("griddepcontrol.wait;" ::: "memory");
+                    bar_expect(t_full, plan.t_bytes);
+                    for (uint32_t o = 0; o < plan.t_bytes; o += kTileRows * 128)
+                        load_2d(&maps.t, t_full, t_base + o, static_cast<int>(o / (kTileRows * 2)),
+                                static_cast<int>(m0));
+                }
                 for (int d = 0; d < count; ++d) {
                     if (!bar_wait(b_empty + 8 * bs, bph ^ 1, ab, 45)) {
                         ok = false;
@@ -594,6 +644,7 @@ __global__ void __launch_bounds__(kThreads)
             }
             if (!ok) {
                 const uint64_t deadline = timer_ns() + kTimeoutNs;
+                if (y_issued > 0 && count > 0) bar_drain(t_full, 0, deadline);
                 for (int i = 0; i < y_issued; ++i) {
                     if (--ys < 0) {
                         ys = plan.y_slots - 1;
@@ -615,7 +666,8 @@ __global__ void __launch_bounds__(kThreads)
             const uint32_t idesc = bf16_idesc(kUnitCols);
             int bs = 0, acc = 0;
             uint32_t bph = 0, aph = 0;
-            const int64_t total = int64_t(u1 - u0) * count;
+            int64_t total = int64_t(u1 - u0) * count;
+            if (total > 0 && !bar_wait(t_full, 0, ab, 46)) total = 0;
             for (int64_t i = 0; i < total; ++i) {
                 if (!bar_wait(b_full + 8 * bs, bph, ab, 46)) break;
                 if (!bar_wait(d_empty + 8 * acc, aph ^ 1, ab, 46)) break;
@@ -660,31 +712,22 @@ __global__ void __launch_bounds__(kThreads)
                 }
                 fence_after();
                 const uint32_t src = tmem + acc * kUnitCols + (static_cast<uint32_t>(quad * 32) << 16);
+                uint32_t f[64];
+                __syncwarp();
+                tmem_ld64(src, f);
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(d_empty + 8 * acc);  // read: back to the MMA thread
+                if (mine == d) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float f[16];
-                    __syncwarp();
-                    tmem_ld16(src + 16 * c, f);
-                    if (c == 3) {  // the accumulator is read: back to the MMA thread
-                        fence_before();
-                        __syncwarp();
-                        if (lane == 0) bar_arrive(d_empty + 8 * acc);
-                    }
-                    if (mine == d) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t at = y + ((32 * c + 16 * h) ^ swz);
-                            uint4 v = ld_shared_16B(at);
-                            uint32_t *w = &v.x;
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const __nv_bfloat162 o =
-                                    __floats2bfloat162_rn(bf16_lo(w[j]) + f[8 * h + 2 * j],
-                                                          bf16_hi(w[j]) + f[8 * h + 2 * j + 1]);
-                                w[j] = *reinterpret_cast<const uint32_t *>(&o);
-                            }
-                            st_shared_16B(at, v);
-                        }
+                    for (int c = 0; c < 8; ++c) {
+                        const uint32_t at = y + ((16 * c) ^ swz);
+                        uint4 v = ld_shared_16B(at);
+                        v.x = add_pair(v.x, f[8 * c], f[8 * c + 1]);
+                        v.y = add_pair(v.y, f[8 * c + 2], f[8 * c + 3]);
+                        v.z = add_pair(v.z, f[8 * c + 4], f[8 * c + 5]);
+                        v.w = add_pair(v.w, f[8 * c + 6], f[8 * c + 7]);
+                        st_shared_16B(at, v);
                     }
                 }
                 if (++acc == kAccs) {
@@ -713,6 +756,7 @@ __global__ void __launch_bounds__(kThreads)
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // this grid never ends before the shrink
     __syncthreads();
     if (warp == 1) {
         if (lane == 0) bar_drain(drain, 0, timer_ns() + kTimeoutNs);  // every MMA has completed
@@ -744,20 +788,39 @@ constexpr int kSms = 148;
 
 int64_t row_tiles(int64_t rows) { return (rows + kTileRows - 1) / kTileRows; }
 
-// K splits of the shrink: enough items for two per SM, none below 8 blocks of
-// 64 (two rings' worth).
+// CTAs of a shrink cluster: of 1, 2, 4 and 8, the number that leaves the SM
+// with the most CTAs the least of K to read, at least 4 blocks of 64 each; of
+// equals the largest that still runs at once, two CTAs per SM keeping more
+// bytes in flight than one.
 int shrink_splits(int64_t rows, int64_t k) {
-    const int64_t want = 2 * kSms / row_tiles(rows), most = (k + 63) / 64 / 8;
-    int64_t s = want < most ? want : most;
-    if (s > 16) s = 16;
-    return s < 1 ? 1 : static_cast<int>(s);
+    const int64_t tiles = row_tiles(rows), blocks = (k + 63) / 64;
+    int best = 1;
+    int64_t best_cost = INT64_MAX;
+    for (int s = 1; s <= 8 && (s == 1 || blocks / s >= 4); s *= 2) {
+        const int64_t cost = (tiles * s + kSms - 1) / kSms * ((blocks + s - 1) / s);
+        if (cost < best_cost || (cost == best_cost && tiles * s <= 2 * kSms)) {
+            best = s;
+            best_cost = cost;
+        }
+    }
+    return best;
 }
 
-// Column ranges of the expand: enough CTAs for two per SM.
-int expand_ranges(int64_t rows, int64_t n) {
-    const int64_t want = (2 * kSms + row_tiles(rows) - 1) / row_tiles(rows);
-    const int64_t most = (n + kUnitCols - 1) / kUnitCols;
-    return static_cast<int>(want < most ? want : most);
+// Column ranges of the expand: the number whose last wave of CTAs wastes
+// least, each range costing about three units of its own to start.
+int expand_ranges(int64_t rows, int64_t n, int64_t rank) {
+    const int64_t tiles = row_tiles(rows), units = (n + kUnitCols - 1) / kUnitCols;
+    const int64_t at_once = rank <= 64 ? 2 * kSms : kSms;
+    int best = 1;
+    int64_t best_cost = INT64_MAX;
+    for (int64_t r = 1; r <= units && r <= 2 * at_once / tiles + 4; ++r) {
+        const int64_t cost = (tiles * r + at_once - 1) / at_once * ((units + r - 1) / r + 3);
+        if (cost < best_cost) {
+            best = static_cast<int>(r);
+            best_cost = cost;
+        }
+    }
+    return best;
 }
 
 template <class K>
@@ -768,25 +831,44 @@ cudaError_t allow_smem(K kernel, uint32_t bytes) {
 
 template <int NB>
 cudaError_t launch_shrink(const ShrinkMaps &maps, const nvfp4_lora_args &p, int splits, float *partial,
-                          int *err, cudaStream_t stream) {
+                          uint16_t *t, int *err, cudaStream_t stream) {
     using Cfg = ShrinkConfig<NB>;
     cudaError_t e = allow_smem(lora_shrink_kernel<NB>, Cfg::SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    lora_shrink_kernel<NB><<<static_cast<unsigned>(row_tiles(p.rows) * splits), kThreads, Cfg::SMEM_BYTES,
-                             stream>>>(maps, p, splits, partial, err);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(splits);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(row_tiles(p.rows) * splits));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, lora_shrink_kernel<NB>, maps, p, splits, partial, t, err);
+}
+
+size_t partial_bytes(int64_t rows, int64_t rank, int splits) {
+    return splits == 1 ? 0 : static_cast<size_t>(splits) * static_cast<size_t>(rows * rank) * sizeof(float);
 }
 
 }  // namespace
 
 size_t lora_tile_workspace_bytes(int64_t rows, int64_t k, int64_t rank) {
-    return static_cast<size_t>(shrink_splits(rows, k)) * static_cast<size_t>(rows) *
-           static_cast<size_t>(rank) * sizeof(float);
+    const TLayout tl(static_cast<int>(rank));
+    return partial_bytes(rows, rank, shrink_splits(rows, k)) +
+           static_cast<size_t>(rows) * static_cast<size_t>(tl.groups) * 128;
 }
 
 cudaError_t launch_lora_tile(const nvfp4_lora_args &p, cudaStream_t stream) {
     int *err = device_error_word();
     if (err == nullptr) return cudaErrorUnknown;
+    const int splits = shrink_splits(p.rows, p.k);
+    const TLayout tl(static_cast<int>(p.rank));
+    float *partial = static_cast<float *>(p.workspace);
+    uint16_t *t = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(p.workspace) +
+                                               partial_bytes(p.rows, p.rank, splits));
     ShrinkMaps sm;
     ExpandMaps em;
     std::memset(&sm, 0, sizeof(sm));
@@ -795,20 +877,27 @@ cudaError_t launch_lora_tile(const nvfp4_lora_args &p, cudaStream_t stream) {
         !encode_map(&sm.a, p.a, p.k, p.slots * p.rank, p.k, static_cast<uint32_t>(p.rank)) ||
         !encode_map(&em.y, p.y, p.n, p.rows, p.y_stride, kTileRows) ||
         !encode_map(&em.b, p.b, p.rank, p.slots * p.n, p.rank, kUnitCols) ||
-        !encode_map(&em.out, p.out, p.n, p.rows, p.out_stride, 32))
+        !encode_map(&em.out, p.out, p.n, p.rows, p.out_stride, 32) ||
+        !encode_map(&em.t, t, tl.groups * 64, p.rows, tl.groups * 64, kTileRows))
         return cudaErrorInvalidValue;
-    const int splits = shrink_splits(p.rows, p.k);
-    float *partial = static_cast<float *>(p.workspace);
-    cudaError_t e = p.rank <= 64 ? launch_shrink<64>(sm, p, splits, partial, err, stream)
-                                 : launch_shrink<128>(sm, p, splits, partial, err, stream);
+    cudaError_t e = p.rank <= 64 ? launch_shrink<64>(sm, p, splits, partial, t, err, stream)
+                                 : launch_shrink<128>(sm, p, splits, partial, t, err, stream);
     if (e != cudaSuccess) return e;
     const ExpandPlan plan = expand_plan(p.rank);
     e = allow_smem(lora_expand_kernel, plan.smem_bytes);
     if (e != cudaSuccess) return e;
-    const int ranges = expand_ranges(p.rows, p.n);
-    lora_expand_kernel<<<static_cast<unsigned>(row_tiles(p.rows) * ranges), kThreads, plan.smem_bytes,
-                         stream>>>(em, p, plan, splits, ranges, partial, err);
-    return cudaGetLastError();
+    const int ranges = expand_ranges(p.rows, p.n, p.rank);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(row_tiles(p.rows) * ranges));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = plan.smem_bytes;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, lora_expand_kernel, em, p, plan, ranges, err);
 }
 
 }  // namespace nvfp4

@@ -683,7 +683,6 @@ __global__ void __launch_bounds__(512, 2)
                 uint4 o[V];
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const int vec = i * T + tx;
                     o[i] = pack4(x[i]);  // zero past the row
                     if (a.out != nullptr && (i == 0 || second))
                         *reinterpret_cast<uint4 *>(op + i * T * 16) = o[i];
