@@ -7,9 +7,9 @@
 // A cluster of CTAs per row.  Each CTA takes a slice of K for every rank (a
 // warp per rank, so a row of A is read in whole lines), the partial sums go to
 // every CTA of the cluster through distributed shared memory, and after one
-// cluster barrier each CTA adds its slice of N: two outputs per thread, whose
-// rows of B are one contiguous piece.  B's slice is asked into L2 before the
-// first product, so its latency passes behind it.
+// cluster barrier each CTA adds its slice of N.  B's slice is asked into L2 as
+// soon as A has arrived, behind the reductions and the barrier; asked for with
+// A, it delays A, which everything waits for.
 // What bounds it: the adapters' bytes, rank * (K + N) * 2 per row, from HBM
 // where rows have adapters of their own and from L2 where they share them.
 #include <cuda_bf16.h>
@@ -26,7 +26,6 @@ namespace {
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kCluster = 8;
-constexpr int kMaxRank = 128;
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -74,63 +73,73 @@ __device__ __forceinline__ float dot8(const float *t, uint4 b, float acc) {
     return fmaf(t[7], bf16_hi(b.w), acc);
 }
 
-__global__ void __launch_bounds__(kRowThreads) __cluster_dims__(kCluster, 1, 1)
+// Rank 16 * R16.  In the second product L lanes share an output's row of B, V
+// 16-byte pieces each, so that a warp reads whole lines; a batch is 32 outputs
+// of a warp, and U batches are in flight at a time.
+template <int R16>
+__global__ void __launch_bounds__(kRowThreads, R16 <= 2 ? 4 : R16 == 4 ? 3 : 2) __cluster_dims__(kCluster, 1, 1)
     lora_rows_kernel(const nvfp4_lora_args p) {
-    __shared__ __align__(16) float part[kCluster][kMaxRank];
-    __shared__ __align__(16) float t[kMaxRank];
+    constexpr int rank = 16 * R16;
+    constexpr int L = R16 == 8 ? 16 : R16 == 4 ? 8 : R16 % 2 == 0 ? 4 : 2;
+    constexpr int V = rank / 8 / L;
+    constexpr int U = rank <= 16 ? 4 : rank <= 48 ? 2 : 1;
+    __shared__ __align__(16) float part[kCluster][rank];
+    __shared__ __align__(16) float t[rank];
     const int64_t row = blockIdx.x / kCluster;
     const int c = static_cast<int>(blockIdx.x % kCluster);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = static_cast<int>(p.rank);
-    const uint32_t *yrow =
-        reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p.y) + row * p.y_stride);
-    uint32_t *orow = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + row * p.out_stride);
-    // This CTA's pairs of outputs.
-    const int64_t pairs = p.n >> 1;
-    const int64_t p0 = pairs * c / kCluster, p1 = pairs * (c + 1) / kCluster;
+    const uint16_t *yrow = static_cast<const uint16_t *>(p.y) + row * p.y_stride;
+    uint16_t *orow = static_cast<uint16_t *>(p.out) + row * p.out_stride;
+    // This CTA's outputs.
+    const int64_t n0 = (p.n >> 3) * c / kCluster * 8, n1 = (p.n >> 3) * (c + 1) / kCluster * 8;
     const int64_t slot = p.row_slot != nullptr ? int64_t(__ldg(p.row_slot + row)) : 0;
     if (slot < 0 || slot >= p.slots) {  // the same in every CTA of the cluster
         if (p.out != p.y)
-            for (int64_t i = p0 + threadIdx.x; i < p1; i += kRowThreads) orow[i] = yrow[i];
+            for (int64_t n = n0 + 8 * threadIdx.x; n < n1; n += 8 * kRowThreads)
+                *reinterpret_cast<uint4 *>(orow + n) = *reinterpret_cast<const uint4 *>(yrow + n);
         return;
     }
     cluster_arrive();  // this CTA runs: its shared memory may be written
     const uint16_t *a = static_cast<const uint16_t *>(p.a) + slot * rank * p.k;
-    const uint8_t *b = static_cast<const uint8_t *>(p.b) + slot * p.n * rank * 2;
-    const int64_t pair_bytes = 4 * int64_t(rank);
-    for (int64_t o = p0 * pair_bytes + threadIdx.x * 128; o < p1 * pair_bytes; o += kRowThreads * 128)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(b + o));
+    const uint8_t *b = static_cast<const uint8_t *>(p.b) + slot * p.n * (rank * 2);
 
-    // t's partial sums over this CTA's slice of K.
+    // t's partial sums over this CTA's slice of K, up to four ranks of a warp
+    // at a time.
     const int64_t nk = p.k >> 3;
     const int64_t k0 = nk * c / kCluster, k1 = nk * (c + 1) / kCluster;
     const uint4 *xrow =
         reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.x) + row * p.x_stride);
-    bool peers_run = false;
-    for (int r = warp; r < rank; r += 2 * kRowWarps) {  // two ranks of a warp at a time
-        const uint4 *a0 = reinterpret_cast<const uint4 *>(a + r * p.k);
-        const uint4 *a1 = reinterpret_cast<const uint4 *>(a + (r + kRowWarps) * p.k);
-        float s0 = 0.0f, s1 = 0.0f;
+    constexpr int kRanks = rank / kRowWarps;  // of a warp: warp, warp + 8, ...
+#pragma unroll 1
+    for (int i0 = 0; i0 < kRanks; i0 += 4) {
+        constexpr int G = kRanks < 4 ? kRanks : 4;
+        float s[G];
+#pragma unroll
+        for (int i = 0; i < G; ++i) s[i] = 0.0f;
 #pragma unroll 2
         for (int64_t k = k0 + lane; k < k1; k += 32) {
             const uint4 xv = __ldg(xrow + k);
-            const uint4 v0 = __ldg(a0 + k), v1 = __ldg(a1 + k);
-            s0 = dot8(xv, v0, s0);
-            s1 = dot8(xv, v1, s1);
-        }
+            uint4 v[G];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, o);
-            s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, o);
+            for (int i = 0; i < G; ++i)
+                if (i0 + i < kRanks)
+                    v[i] = __ldg(reinterpret_cast<const uint4 *>(a + (warp + (i0 + i) * kRowWarps) * p.k) + k);
+#pragma unroll
+            for (int i = 0; i < G; ++i)
+                if (i0 + i < kRanks) s[i] = dot8(xv, v[i], s[i]);
         }
-        if (!peers_run) {
-            cluster_wait();
-            peers_run = true;
-        }
-        if (lane < kCluster) {
-            st_cluster_f32(&part[c][r], lane, s0);
-            st_cluster_f32(&part[c][r + kRowWarps], lane, s1);
-        }
+        if (i0 + 4 >= kRanks)  // A is here: HBM's next work, behind the reductions and the barrier
+            for (int64_t o = n0 * (rank * 2) + threadIdx.x * 128; o < n1 * (rank * 2); o += kRowThreads * 128)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(b + o), "f"(s[0]));
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) s[i] += __shfl_xor_sync(0xFFFFFFFFu, s[i], o);
+        if (i0 == 0) cluster_wait();
+        if (lane < kCluster)
+#pragma unroll
+            for (int i = 0; i < G; ++i)
+                if (i0 + i < kRanks) st_cluster_f32(&part[c][warp + (i0 + i) * kRowWarps], lane, s[i]);
     }
     cluster_arrive();
     cluster_wait();
@@ -142,20 +151,58 @@ __global__ void __launch_bounds__(kRowThreads) __cluster_dims__(kCluster, 1, 1)
     }
     __syncthreads();
 
-    const int vecs = rank >> 3;
-    for (int64_t i = p0 + threadIdx.x; i < p1; i += kRowThreads) {
-        const uint4 *b0 = reinterpret_cast<const uint4 *>(b + i * pair_bytes);
-        const uint4 *b1 = b0 + vecs;
-        float lo = 0.0f, hi = 0.0f;
-#pragma unroll 4
-        for (int v = 0; v < vecs; ++v) {
-            lo = dot8(t + 8 * v, __ldg(b0 + v), lo);
-            hi = dot8(t + 8 * v, __ldg(b1 + v), hi);
+    const int l = lane % L, group = lane / L;
+    float tv[V][8];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) tv[v][j] = t[(v * L + l) * 8 + j];
+    for (int64_t base = n0 + warp * (32 * U); base < n1; base += kRowWarps * 32 * U) {
+        uint4 bv[U][L][V];
+        uint16_t yv[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int j = 0; j < L; ++j) {
+                const int64_t n = base + u * 32 + j * (32 / L) + group;
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (n < n1)
+                        bv[u][j][v] = __ldg(reinterpret_cast<const uint4 *>(b + n * (rank * 2)) + v * L + l);
+            }
+            const int64_t n = base + u * 32 + l * (32 / L) + group;
+            if (n < n1) yv[u] = yrow[n];
         }
-        const uint32_t yv = yrow[i];
-        const __nv_bfloat162 o = __floats2bfloat162_rn(bf16_lo(yv) + lo, bf16_hi(yv) + hi);
-        orow[i] = *reinterpret_cast<const uint32_t *>(&o);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float acc[L];
+#pragma unroll
+            for (int j = 0; j < L; ++j) {
+                acc[j] = 0.0f;
+#pragma unroll
+                for (int v = 0; v < V; ++v) acc[j] = dot8(tv[v], bv[u][j][v], acc[j]);
+            }
+            // The L lanes' sums meet, each lane keeping the output of its number.
+#pragma unroll
+            for (int o = L / 2; o > 0; o >>= 1)
+#pragma unroll
+                for (int j = 0; j < o; ++j) {
+                    const bool upper = l & o;
+                    const float other = __shfl_xor_sync(0xFFFFFFFFu, upper ? acc[j] : acc[j + o], o);
+                    acc[j] = (upper ? acc[j + o] : acc[j]) + other;
+                }
+            const int64_t n = base + u * 32 + l * (32 / L) + group;
+            if (n < n1)
+                orow[n] = __bfloat16_as_ushort(
+                    __float2bfloat16_rn(__uint_as_float(static_cast<uint32_t>(yv[u]) << 16) + acc[0]));
+        }
     }
+}
+
+template <int R16>
+cudaError_t launch_rows(const nvfp4_lora_args &p, cudaStream_t stream) {
+    lora_rows_kernel<R16><<<static_cast<unsigned>(p.rows * kCluster), kRowThreads, 0, stream>>>(p);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -170,8 +217,16 @@ size_t lora_workspace_bytes(int64_t rows, int64_t k, int64_t n, int64_t rank) {
 
 cudaError_t launch_lora(const nvfp4_lora_args &p, cudaStream_t stream) {
     if (p.rows >= kTileFromRows) return launch_lora_tile(p, stream);
-    lora_rows_kernel<<<static_cast<unsigned>(p.rows * kCluster), kRowThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    switch (p.rank / 16) {
+        case 1: return launch_rows<1>(p, stream);
+        case 2: return launch_rows<2>(p, stream);
+        case 3: return launch_rows<3>(p, stream);
+        case 4: return launch_rows<4>(p, stream);
+        case 5: return launch_rows<5>(p, stream);
+        case 6: return launch_rows<6>(p, stream);
+        case 7: return launch_rows<7>(p, stream);
+        default: return launch_rows<8>(p, stream);
+    }
 }
 
 }  // namespace nvfp4

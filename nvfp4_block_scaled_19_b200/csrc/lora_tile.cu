@@ -51,6 +51,7 @@ constexpr int kThreads = 192;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr uint32_t kXBytes = kTileRows * 128;  // 128 rows x 64 bf16
 constexpr uint32_t kUnitCols = 64;
+constexpr int kMaxSplits = 8;  // CTAs of a shrink cluster, over K
 
 // ---------------------------------------------------------------- PTX
 
@@ -336,6 +337,9 @@ __global__ void __launch_bounds__(kThreads)
     const int k_blocks = static_cast<int>((p.k + 63) / 64);
     const int kb0 = static_cast<int>(int64_t(k_blocks) * split / splits);
     const int kb1 = static_cast<int>(int64_t(k_blocks) * (split + 1) / splits);
+    // Tiles start at different places of K, so that the many that share an
+    // adapter do not all ask for the same lines of it at the same moment.
+    const int kb_first = kb0 + tile % (kb1 - kb0);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < Cfg::STAGES; ++s) {
@@ -374,7 +378,7 @@ __global__ void __launch_bounds__(kThreads)
             bool ok = true;
             for (int q = 0; q < passes && ok; ++q) {
                 const int d0 = q * group, d1 = min(ts.count, d0 + group);
-                for (int kb = kb0; kb < kb1; ++kb) {
+                for (int i = 0, kb = kb_first; i < kb1 - kb0; ++i, kb = kb + 1 < kb1 ? kb + 1 : kb0) {
                     if (!bar_wait(empty + 8 * stage, phase ^ 1, ab, 40)) {
                         ok = false;
                         break;
@@ -493,16 +497,22 @@ __global__ void __launch_bounds__(kThreads)
         const int row = split * share + i / eights, r = (i % eights) * 8;
         const int d = ts.row[row];
         if (d < 0) continue;
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
         const float *src = partial + (m0 + row) * rank + r;
-        for (int s = 0; s < splits; ++s, src += p.rows * rank) {
-            const float4 a = *reinterpret_cast<const float4 *>(src);
-            const float4 b = *reinterpret_cast<const float4 *>(src + 4);
-            v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-            v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
-        }
+        float4 w[kMaxSplits][2];  // asked for together
+#pragma unroll
+        for (int s = 0; s < kMaxSplits; ++s)
+            if (s < splits) {
+                const float4 *o = reinterpret_cast<const float4 *>(src + s * p.rows * rank);
+                w[s][0] = o[0];
+                w[s][1] = o[1];
+            }
+        float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int s = 0; s < kMaxSplits; ++s)
+            if (s < splits) {
+                v[0] += w[s][0].x; v[1] += w[s][0].y; v[2] += w[s][0].z; v[3] += w[s][0].w;
+                v[4] += w[s][1].x; v[5] += w[s][1].y; v[6] += w[s][1].z; v[7] += w[s][1].w;
+            }
         const float c = __ldg(p.scale + ts.list[d]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] *= c;
@@ -563,6 +573,7 @@ __global__ void __launch_bounds__(kThreads)
     const int units = static_cast<int>((p.n + kUnitCols - 1) / kUnitCols);
     const int u0 = static_cast<int>(int64_t(units) * range / ranges);
     const int u1 = static_cast<int>(int64_t(units) * (range + 1) / ranges);
+    const int u_first = u0 + tile % (u1 - u0);  // as in the shrink
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < plan.y_slots; ++s) {
@@ -605,7 +616,7 @@ __global__ void __launch_bounds__(kThreads)
             int ys = 0, bs = 0, y_issued = 0, b_issued = 0;
             uint32_t yph = 0, bph = 0;
             bool ok = true;
-            for (int u = u0; u < u1 && ok; ++u) {
+            for (int i = 0, u = u_first; i < u1 - u0 && ok; ++i, u = u + 1 < u1 ? u + 1 : u0) {
                 if (!bar_wait(y_empty + 8 * ys, yph ^ 1, ab, 44)) {
                     ok = false;
                     break;
@@ -618,7 +629,7 @@ __global__ void __launch_bounds__(kThreads)
                     ys = 0;
                     yph ^= 1;
                 }
-                if (u == u0 && count > 0) {  // the shrink's result
+                if (i == 0 && count > 0) {  // the shrink's result
                     asm volatile("griddepcontrol.wait;" ::: "memory");
                     bar_expect(t_full, plan.t_bytes);
                     for (uint32_t o = 0; o < plan.t_bytes; o += kTileRows * 128)
@@ -702,7 +713,7 @@ __global__ void __launch_bounds__(kThreads)
         int ys = 0, acc = 0, prev = -1;
         uint32_t yph = 0, aph = 0;
         bool ok = true;
-        for (int u = u0; u < u1 && ok; ++u) {
+        for (int i = 0, u = u_first; i < u1 - u0 && ok; ++i, u = u + 1 < u1 ? u + 1 : u0) {
             if (!bar_wait_warp(y_full + 8 * ys, yph, ab, 47)) break;
             const uint32_t y = y_ring + ys * kYBytes + row * 128;
             for (int d = 0; d < count; ++d) {
@@ -796,7 +807,7 @@ int shrink_splits(int64_t rows, int64_t k) {
     const int64_t tiles = row_tiles(rows), blocks = (k + 63) / 64;
     int best = 1;
     int64_t best_cost = INT64_MAX;
-    for (int s = 1; s <= 8 && (s == 1 || blocks / s >= 4); s *= 2) {
+    for (int s = 1; s <= kMaxSplits && (s == 1 || blocks / s >= 4); s *= 2) {
         const int64_t cost = (tiles * s + kSms - 1) / kSms * ((blocks + s - 1) / s);
         if (cost < best_cost || (cost == best_cost && tiles * s <= 2 * kSms)) {
             best = s;
