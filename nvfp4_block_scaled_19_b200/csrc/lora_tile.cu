@@ -4,11 +4,13 @@
 // lora_shrink_kernel   t[m] = scale[s] * A[s] x[m].
 //   A cluster of `splits` CTAs per row tile, each over its share of K.  A stage
 //   is the tile's 128 x 64 piece of x and, side by side as one B operand, the
-//   matching rank x 64 pieces of up to G = NB / rank different adapters, so a
+//   matching rank x 64 pieces of up to G = 256 / rank different adapters, so a
 //   tile whose rows belong to G requests still reads x once; each row's
 //   epilogue thread keeps its own adapter's columns.  The splits' fp32 sums meet
-//   in the workspace: after a cluster barrier each CTA adds up its share of the
-//   rows, in the order of the splits, so the result does not depend on timing.
+//   through distributed shared memory (in the workspace where a tile has more
+//   adapters than a pass takes, as the ring is then still in use): after a
+//   cluster barrier each CTA adds up its share of the rows, in the order of the
+//   splits, so the result does not depend on timing.
 //   t is written as the sum of two bf16 (hi + lo, 16 mantissa bits), as the
 //   expand's MMA takes it.
 // lora_expand_kernel   out[m][n] = bf16(y[m][n] + B[s] t[m]).
@@ -50,7 +52,6 @@ constexpr int kTileRows = 128;
 constexpr int kThreads = 192;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr uint32_t kXBytes = kTileRows * 128;  // 128 rows x 64 bf16
-constexpr uint32_t kUnitCols = 64;
 constexpr int kMaxSplits = 8;  // CTAs of a shrink cluster, over K
 
 // ---------------------------------------------------------------- PTX
@@ -98,11 +99,16 @@ struct Abort {
 
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const Abort &ab, int tag) {
     if (bar_try(bar, parity)) return true;
-    const uint64_t t0 = timer_ns();
+    uint64_t t0 = 0;
     while (true) {
-        if (bar_try(bar, parity)) return true;
+        // The clock that bounds the wait is slow to read: between many tries.
+#pragma unroll 1
+        for (int i = 0; i < 256; ++i)
+            if (bar_try(bar, parity)) return true;
         if (*ab.flag) return false;
-        if (timer_ns() - t0 > kTimeoutNs) {
+        const uint64_t now = timer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > kTimeoutNs) {
             if (atomicCAS(&ab.err[0], 0, NVFP4_ERR_TIMEOUT) == 0) ab.err[1] = tag;
             *ab.flag = 1;
             return false;
@@ -129,6 +135,12 @@ __device__ __forceinline__ void load_2d(const CUtensorMap *m, uint32_t bar, uint
         " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
         "l"(m), "r"(bar), "r"(x), "r"(y)
         : "memory");
+}
+
+__device__ __forceinline__ void prefetch_2d(const CUtensorMap *m, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(m), "r"(x),
+                 "r"(y)
+                 : "memory");
 }
 
 __device__ __forceinline__ void store_2d(const CUtensorMap *m, uint32_t src, int x, int y) {
@@ -222,6 +234,19 @@ __device__ __forceinline__ void st_shared_16B(uint32_t a, uint4 v) {
                  : "memory");
 }
 
+// 16 bytes at this CTA's shared address `a`, of CTA `rank` of the cluster.
+__device__ __forceinline__ float4 ld_cluster_16B(uint32_t a, uint32_t rank) {
+    float4 v;
+    asm volatile(
+        "{\n\t.reg .b32 r;\n\t"
+        "mapa.shared::cluster.u32 r, %4, %5;\n\t"
+        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [r];\n\t}\n"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(a), "r"(rank)
+        : "memory");
+    return v;
+}
+
 // ---------------------------------------------------------------- the tile's adapters
 
 struct TileSlots {
@@ -308,27 +333,26 @@ struct alignas(64) ExpandMaps {
 
 // ---------------------------------------------------------------- shrink
 
-template <int NB>
-struct ShrinkConfig {
-    static constexpr int STAGES = NB == 64 ? 4 : 3;  // two CTAs of ~96 KB per SM
-    static constexpr uint32_t STAGE_BYTES = kXBytes + NB * 128;
-    static constexpr uint32_t SMEM_BYTES = STAGES * STAGE_BYTES + 1024;
-    static constexpr uint32_t TMEM_COLS = 2 * NB;  // two accumulators
-};
+constexpr int kMaxStages = 8;
+constexpr int kAccCols = 256;  // tensor memory of a CTA of either kernel: two fit an SM
 
-template <int NB>
+// Rings of 96 KB (two CTAs per SM) or 192 KB (one, where the grid has no more
+// and no clusters: those do not fill every SM), cut into stages of the tile's own size: x's piece and those of the adapters of
+// a pass.
+constexpr uint32_t kSmallRing = 96 * 1024, kLargeRing = 192 * 1024;
+
 __global__ void __launch_bounds__(kThreads)
     lora_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const nvfp4_lora_args p,
-                       const int splits, float *partial, uint16_t *t, int *err) {
-    using Cfg = ShrinkConfig<NB>;
+                       const int splits, const uint32_t ring_bytes, float *partial, uint16_t *t,
+                       int *err) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ TileSlots ts;
-    __shared__ __align__(8) uint64_t bars[2 * Cfg::STAGES + 5];
+    __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 3];
     __shared__ uint32_t tmem_holder;
     __shared__ int abort_flag;
     const uint32_t ring = (s32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t full = s32(bars), empty = full + 8 * Cfg::STAGES;
-    const uint32_t acc_full = empty + 8 * Cfg::STAGES, acc_empty = acc_full + 16, drain = acc_empty + 16;
+    const uint32_t full = s32(bars), empty = full + 8 * kMaxStages;
+    const uint32_t acc_full = empty + 8 * kMaxStages, acc_empty = acc_full + 8, drain = acc_empty + 8;
     const Abort ab{&abort_flag, err};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tile = blockIdx.x / splits, split = blockIdx.x % splits;
@@ -337,30 +361,27 @@ __global__ void __launch_bounds__(kThreads)
     const int k_blocks = static_cast<int>((p.k + 63) / 64);
     const int kb0 = static_cast<int>(int64_t(k_blocks) * split / splits);
     const int kb1 = static_cast<int>(int64_t(k_blocks) * (split + 1) / splits);
-    // Tiles start at different places of K, so that the many that share an
-    // adapter do not all ask for the same lines of it at the same moment.
-    const int kb_first = kb0 + tile % (kb1 - kb0);
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < Cfg::STAGES; ++s) {
+        for (int s = 0; s < kMaxStages; ++s) {
             bar_init(full + 8 * s, 1);
             bar_init(empty + 8 * s, 1);
         }
-        for (int s = 0; s < 2; ++s) {
-            bar_init(acc_full + 8 * s, 1);
-            bar_init(acc_empty + 8 * s, 4);
-        }
+        bar_init(acc_full, 1);
+        bar_init(acc_empty, 4);
         bar_init(drain, 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x == 32)  // the first of x on its way while the adapters are found
+        for (int kb = kb0; kb < min(kb0 + 4, kb1); ++kb)
+            prefetch_2d(&maps.x, kb * 64, static_cast<int>(m0));
     find_slots(ts, p, m0);
     if (ts.count == 0) return;  // no row has an adapter (the same in the whole cluster)
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          s32(&tmem_holder)),
-                     "r"(Cfg::TMEM_COLS)
+                     "r"(kAccCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -368,8 +389,12 @@ __global__ void __launch_bounds__(kThreads)
     __syncthreads();
     fence_after();
     const uint32_t tmem = tmem_holder;
-    const int group = NB / rank;  // adapters per pass over x
+    // The expand may start its prologue once every CTA here holds its tensor memory.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int group = min(kAccCols / rank, ts.count);  // adapters per pass over x
     const int passes = (ts.count + group - 1) / group;
+    const uint32_t stage_bytes = kXBytes + group * rank * 128;  // at most 48 KB
+    const int stages = min(kMaxStages, static_cast<int>(ring_bytes / stage_bytes));
 
     if (warp == 0) {
         if (lane == 0) {
@@ -378,19 +403,19 @@ __global__ void __launch_bounds__(kThreads)
             bool ok = true;
             for (int q = 0; q < passes && ok; ++q) {
                 const int d0 = q * group, d1 = min(ts.count, d0 + group);
-                for (int i = 0, kb = kb_first; i < kb1 - kb0; ++i, kb = kb + 1 < kb1 ? kb + 1 : kb0) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!bar_wait(empty + 8 * stage, phase ^ 1, ab, 40)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t dst = ring + stage * Cfg::STAGE_BYTES, bar = full + 8 * stage;
+                    const uint32_t dst = ring + stage * stage_bytes, bar = full + 8 * stage;
                     bar_expect(bar, kXBytes + (d1 - d0) * rank * 128);
                     load_2d(&maps.x, bar, dst, kb * 64, static_cast<int>(m0));
                     for (int d = d0; d < d1; ++d)
                         load_2d(&maps.a, bar, dst + kXBytes + (d - d0) * rank * 128, kb * 64,
                                 ts.list[d] * rank);
-                    if (issued < Cfg::STAGES) ++issued;
-                    if (++stage == Cfg::STAGES) {
+                    if (issued < stages) ++issued;
+                    if (++stage == stages) {
                         stage = 0;
                         phase ^= 1;
                     }
@@ -400,7 +425,7 @@ __global__ void __launch_bounds__(kThreads)
                 const uint64_t deadline = timer_ns() + kTimeoutNs;
                 for (int i = 0; i < issued; ++i) {
                     if (--stage < 0) {
-                        stage = Cfg::STAGES - 1;
+                        stage = stages - 1;
                         phase ^= 1;
                     }
                     bar_drain(full + 8 * stage, phase, deadline);
@@ -415,8 +440,7 @@ __global__ void __launch_bounds__(kThreads)
             for (int q = 0; q < passes && ok; ++q) {
                 const int d0 = q * group, d1 = min(ts.count, d0 + group);
                 const uint32_t idesc = bf16_idesc((d1 - d0) * rank);
-                const uint32_t acc = tmem + (q & 1) * NB;
-                if (!bar_wait(acc_empty + 8 * (q & 1), ((q >> 1) & 1) ^ 1, ab, 41)) {
+                if (!bar_wait(acc_empty, (q & 1) ^ 1, ab, 41)) {
                     ok = false;
                     break;
                 }
@@ -427,18 +451,18 @@ __global__ void __launch_bounds__(kThreads)
                         break;
                     }
                     fence_after();
-                    const uint64_t a = operand_desc(ring + stage * Cfg::STAGE_BYTES);
-                    const uint64_t b = operand_desc(ring + stage * Cfg::STAGE_BYTES + kXBytes);
+                    const uint64_t a = operand_desc(ring + stage * stage_bytes);
+                    const uint64_t b = operand_desc(ring + stage * stage_bytes + kXBytes);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        mma_bf16(acc, a + 2 * j, b + 2 * j, idesc, (kb > kb0 || j > 0) ? 1u : 0u);
+                        mma_bf16(tmem, a + 2 * j, b + 2 * j, idesc, (kb > kb0 || j > 0) ? 1u : 0u);
                     mma_commit(empty + 8 * stage);
-                    if (++stage == Cfg::STAGES) {
+                    if (++stage == stages) {
                         stage = 0;
                         phase ^= 1;
                     }
                 }
-                if (ok) mma_commit(acc_full + 8 * (q & 1));
+                if (ok) mma_commit(acc_full);
             }
             mma_commit(drain);
         }
@@ -452,9 +476,9 @@ __global__ void __launch_bounds__(kThreads)
         const float c = mine >= 0 ? __ldg(p.scale + ts.list[mine]) : 0.0f;
         for (int q = 0; q < passes; ++q) {
             const int d0 = q * group, d1 = min(ts.count, d0 + group);
-            if (!bar_wait_warp(acc_full + 8 * (q & 1), (q >> 1) & 1, ab, 43)) break;
+            if (!bar_wait_warp(acc_full, q & 1, ab, 43)) break;
             fence_after();
-            const uint32_t acc = tmem + (q & 1) * NB + (static_cast<uint32_t>(quad * 32) << 16);
+            const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16);
             for (int d = d0; d < d1; ++d)
                 for (int r = 0; r < rank; r += 16) {
                     float f[16];
@@ -466,6 +490,12 @@ __global__ void __launch_bounds__(kThreads)
                         for (int j = 0; j < 16; ++j) f[j] *= c;
                         store_t8(f, tdst + r, tdst + tl.lo_at + r);
                         store_t8(f + 8, tdst + r + 8, tdst + tl.lo_at + r + 8);
+                    } else if (passes == 1) {  // the ring is free: every stage has been multiplied
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            st_shared_16B(ring + (((r >> 2) + j) * kTileRows + row) * 16,
+                                          make_uint4(__float_as_uint(f[4 * j]), __float_as_uint(f[4 * j + 1]),
+                                                     __float_as_uint(f[4 * j + 2]), __float_as_uint(f[4 * j + 3])));
                     } else {
                         float4 *o = reinterpret_cast<float4 *>(dst + r);
 #pragma unroll
@@ -475,7 +505,7 @@ __global__ void __launch_bounds__(kThreads)
                 }
             fence_before();
             __syncwarp();
-            if (lane == 0) bar_arrive(acc_empty + 8 * (q & 1));
+            if (lane == 0) bar_arrive(acc_empty);
         }
     }
     __syncthreads();
@@ -483,7 +513,7 @@ __global__ void __launch_bounds__(kThreads)
         if (lane == 0) bar_drain(drain, 0, timer_ns() + kTimeoutNs);  // every MMA has completed
         __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                     "r"(Cfg::TMEM_COLS)
+                     "r"(kAccCols)
                      : "memory");
     }
     if (splits == 1) return;
@@ -492,20 +522,30 @@ __global__ void __launch_bounds__(kThreads)
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                      : "memory");
     const TLayout tl(rank);
-    const int eights = rank >> 3, share = kTileRows / splits;
-    for (int i = threadIdx.x; i < share * eights; i += kThreads) {
-        const int row = split * share + i / eights, r = (i % eights) * 8;
+    const int share = kTileRows / splits;
+    for (int i = threadIdx.x; i < share * (rank >> 3); i += kThreads) {
+        const int row = split * share + i % share, r = i / share * 8;
         const int d = ts.row[row];
         if (d < 0) continue;
-        const float *src = partial + (m0 + row) * rank + r;
         float4 w[kMaxSplits][2];  // asked for together
+        if (passes == 1) {
+            const uint32_t at = ring + ((r >> 2) * kTileRows + row) * 16;
 #pragma unroll
-        for (int s = 0; s < kMaxSplits; ++s)
-            if (s < splits) {
-                const float4 *o = reinterpret_cast<const float4 *>(src + s * p.rows * rank);
-                w[s][0] = o[0];
-                w[s][1] = o[1];
-            }
+            for (int s = 0; s < kMaxSplits; ++s)
+                if (s < splits) {
+                    w[s][0] = ld_cluster_16B(at, s);
+                    w[s][1] = ld_cluster_16B(at + kTileRows * 16, s);
+                }
+        } else {
+            const float *src = partial + (m0 + row) * rank + r;
+#pragma unroll
+            for (int s = 0; s < kMaxSplits; ++s)
+                if (s < splits) {
+                    const float4 *o = reinterpret_cast<const float4 *>(src + s * p.rows * rank);
+                    w[s][0] = o[0];
+                    w[s][1] = o[1];
+                }
+        }
         float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int s = 0; s < kMaxSplits; ++s)
@@ -519,41 +559,55 @@ __global__ void __launch_bounds__(kThreads)
         uint16_t *o = t + (m0 + row) * (tl.groups * 64) + r;
         store_t8(v, o, o + tl.lo_at);
     }
+    // No CTA of the cluster leaves while another reads its shared memory.
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                     : "memory");
 }
 
 // ---------------------------------------------------------------- expand
 
-// Shared-memory plan of one expand launch, made on the host from the rank.
+// Shared-memory plan of an expand launch, from the rank.  Up to rank 64 two CTAs
+// fit an SM (104 KB each) on units of 64 columns; above, t alone is 64 KB, and
+// one CTA takes units of 128: an MMA of 64 columns costs the tensor core about
+// as much as one of 128.
 struct ExpandPlan {
     int y_slots, b_slots;     // ring depths
-    uint32_t b_bytes;         // one B piece: 64 rows x (64 ranks x chunks)
+    uint32_t b_bytes;         // a unit's B: `unit` rows x (64 ranks x chunks)
     uint32_t lo_offset;       // bytes from t's hi part to its lo part
     uint32_t t_bytes;
     int chunks;               // 64-rank chunks
     uint32_t smem_bytes;
 };
 
-constexpr int kMaxYSlots = 6, kMaxBSlots = 4;
-constexpr uint32_t kYBytes = kTileRows * 128;  // 128 rows x 64 columns
-constexpr int kAccs = 4;                       // accumulators of 64 columns
+constexpr int kMaxYSlots = 4, kMaxBSlots = 3;
+constexpr uint32_t kBoxBytes = kTileRows * 128;  // 128 rows x 64 columns
+
+constexpr int kUnitsPerCta = 32;
+
+int expand_unit(int64_t rank) { return rank <= 64 ? 64 : 128; }
 
 ExpandPlan expand_plan(int64_t rank) {
+    const TLayout tl(static_cast<int>(rank));
+    const int unit = expand_unit(rank);
     ExpandPlan e;
     e.chunks = rank > 64 ? 2 : 1;
-    e.b_bytes = e.chunks * 64 * 128;
-    // Up to rank 32, hi and lo share one 128-byte row.
-    e.lo_offset = rank <= 32 ? 64 : e.chunks * kTileRows * 128;
-    e.t_bytes = (rank <= 32 ? 1 : 2 * e.chunks) * kTileRows * 128;
-    // Two CTAs per SM up to rank 64 (at most 113 KB each), one above.
-    e.y_slots = rank <= 32 ? 4 : rank <= 64 ? 3 : 5;
-    e.b_slots = rank <= 64 ? 3 : 4;
-    e.smem_bytes = e.t_bytes + e.y_slots * kYBytes + e.b_slots * e.b_bytes + 1024;
+    e.b_bytes = e.chunks * unit * 128;
+    e.lo_offset = rank <= 32 ? 64 : tl.groups / 2 * kBoxBytes;
+    e.t_bytes = tl.groups * kBoxBytes;
+    e.y_slots = rank <= 32 ? 4 : 3;
+    e.b_slots = rank <= 64 ? 3 : 2;
+    e.smem_bytes = e.t_bytes + e.y_slots * (unit / 64 * kBoxBytes) + e.b_slots * e.b_bytes + 1024;
     return e;
 }
 
+// The launch's units, row tile by row tile, are dealt out evenly: CTA i of G
+// takes those from units * i / G on, which are parts of one or a few tiles.
+template <int kUnit>
 __global__ void __launch_bounds__(kThreads)
     lora_expand_kernel(const __grid_constant__ ExpandMaps maps, const nvfp4_lora_args p,
-                       const ExpandPlan plan, const int ranges, int *err) {
+                       const ExpandPlan plan, int *err) {
+    constexpr uint32_t kYBytes = kUnit / 64 * kBoxBytes;
+    constexpr int kAccs = kAccCols / kUnit;
     extern __shared__ uint8_t smem_raw[];
     __shared__ TileSlots ts;
     __shared__ __align__(8) uint64_t bars[2 * kMaxYSlots + 2 * kMaxBSlots + 2 * kAccs + 2];
@@ -567,13 +621,10 @@ __global__ void __launch_bounds__(kThreads)
     const uint32_t t_full = d_empty + 8 * kAccs, drain = t_full + 8;
     const Abort ab{&abort_flag, err};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tile = blockIdx.x / ranges, range = blockIdx.x % ranges;
-    const int64_t m0 = int64_t(tile) * kTileRows;
     const int rank = static_cast<int>(p.rank);
-    const int units = static_cast<int>((p.n + kUnitCols - 1) / kUnitCols);
-    const int u0 = static_cast<int>(int64_t(units) * range / ranges);
-    const int u1 = static_cast<int>(int64_t(units) * (range + 1) / ranges);
-    const int u_first = u0 + tile % (u1 - u0);  // as in the shrink
+    const int units = static_cast<int>((p.n + kUnit - 1) / kUnit);  // of a row tile
+    const int64_t tiles = (p.rows + kTileRows - 1) / kTileRows, total = tiles * units;
+    const int64_t g0 = total * blockIdx.x / gridDim.x, g1 = total * (blockIdx.x + 1) / gridDim.x;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < plan.y_slots; ++s) {
@@ -593,15 +644,10 @@ __global__ void __launch_bounds__(kThreads)
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    find_slots(ts, p, m0);
-    if (ts.count == 0 && p.out == p.y) {  // nothing to add and nothing to copy
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        return;
-    }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          s32(&tmem_holder)),
-                     "r"(kAccs * kUnitCols)
+                     "r"(kAccCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -609,173 +655,205 @@ __global__ void __launch_bounds__(kThreads)
     __syncthreads();
     fence_after();
     const uint32_t tmem = tmem_holder;
-    const int count = ts.count;
 
-    if (warp == 0) {
-        if (lane == 0) {
-            int ys = 0, bs = 0, y_issued = 0, b_issued = 0;
-            uint32_t yph = 0, bph = 0;
-            bool ok = true;
-            for (int i = 0, u = u_first; i < u1 - u0 && ok; ++i, u = u + 1 < u1 ? u + 1 : u0) {
-                if (!bar_wait(y_empty + 8 * ys, yph ^ 1, ab, 44)) {
-                    ok = false;
-                    break;
-                }
-                bar_expect(y_full + 8 * ys, kYBytes);
-                load_2d(&maps.y, y_full + 8 * ys, y_ring + ys * kYBytes, u * kUnitCols,
-                        static_cast<int>(m0));
-                if (y_issued < plan.y_slots) ++y_issued;
-                if (++ys == plan.y_slots) {
-                    ys = 0;
-                    yph ^= 1;
-                }
-                if (i == 0 && count > 0) {  // the shrink's result
-                    asm volatile("griddepcontrol.wait;" ::: "memory");
-                    bar_expect(t_full, plan.t_bytes);
-                    for (uint32_t o = 0; o < plan.t_bytes; o += kTileRows * 128)
-                        load_2d(&maps.t, t_full, t_base + o, static_cast<int>(o / (kTileRows * 2)),
-                                static_cast<int>(m0));
-                }
-                for (int d = 0; d < count; ++d) {
-                    if (!bar_wait(b_empty + 8 * bs, bph ^ 1, ab, 45)) {
-                        ok = false;
-                        break;
+    // Ring positions, of whichever role the thread has; they go on from tile
+    // to tile.
+    int ys = 0, bs = 0, acc = 0, y_issued = 0, b_issued = 0, prev = -1;
+    uint32_t yph = 0, bph = 0, aph = 0, tph = 0;
+    bool waited = false, t_issued = false;
+
+    for (int64_t g = g0; g < g1;) {
+        const int64_t tile = g / units;
+        const int u0 = static_cast<int>(g - tile * units);
+        const int u1 = static_cast<int>(min(g1 - tile * units, int64_t(units)));
+        const int64_t m0 = tile * kTileRows;
+        g += u1 - u0;
+        find_slots(ts, p, m0);  // begins after every role's end of the last tile, see below
+        const int count = ts.count;
+        if (count == 0 && p.out == p.y) continue;  // nothing to add and nothing to copy
+
+        if (warp == 0) {
+            if (lane == 0) {
+                bool ok = true;
+                for (int u = u0; u < u1 && ok; ++u) {
+                    if (!bar_wait(y_empty + 8 * ys, yph ^ 1, ab, 44)) break;
+                    bar_expect(y_full + 8 * ys, kYBytes);
+#pragma unroll
+                    for (int h = 0; h < kUnit; h += 64)
+                        load_2d(&maps.y, y_full + 8 * ys, y_ring + ys * kYBytes + h * (kTileRows * 2),
+                                u * kUnit + h, static_cast<int>(m0));
+                    if (y_issued < plan.y_slots) ++y_issued;
+                    if (++ys == plan.y_slots) {
+                        ys = 0;
+                        yph ^= 1;
                     }
-                    bar_expect(b_full + 8 * bs, plan.b_bytes);
-                    const int row = static_cast<int>(ts.list[d] * p.n + u * kUnitCols);
-                    for (int c = 0; c < plan.chunks; ++c)
-                        load_2d(&maps.b, b_full + 8 * bs, b_ring + bs * plan.b_bytes + c * 8192, c * 64,
-                                row);
-                    if (b_issued < plan.b_slots) ++b_issued;
+                    for (int d = 0; d < count; ++d) {
+                        if (!bar_wait(b_empty + 8 * bs, bph ^ 1, ab, 45)) {
+                            ok = false;
+                            break;
+                        }
+                        bar_expect(b_full + 8 * bs, plan.b_bytes);
+                        const int row = static_cast<int>(ts.list[d] * p.n + u * kUnit);
+                        for (int c = 0; c < plan.chunks; ++c)
+                            load_2d(&maps.b, b_full + 8 * bs, b_ring + bs * plan.b_bytes + c * (kUnit * 128),
+                                    c * 64, row);
+                        if (b_issued < plan.b_slots) ++b_issued;
+                        if (++bs == plan.b_slots) {
+                            bs = 0;
+                            bph ^= 1;
+                        }
+                    }
+                }
+            }
+        } else if (warp == 1) {
+            if (lane == 0 && count > 0) {
+                // t, the one thing here that waits for the shrink.
+                if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+                waited = true;
+                bar_expect(t_full, plan.t_bytes);
+                for (uint32_t o = 0; o < plan.t_bytes; o += kBoxBytes)
+                    load_2d(&maps.t, t_full, t_base + o, static_cast<int>(o / (kTileRows * 2)),
+                            static_cast<int>(m0));
+                t_issued = true;
+                constexpr uint32_t n_field = static_cast<uint32_t>(kUnit >> 3) << 17;
+                const uint32_t idesc = bf16_idesc(0) | n_field;
+                int64_t left = int64_t(u1 - u0) * count;
+                if (!bar_wait(t_full, tph, ab, 46)) left = 0;
+                if (left > 0) {
+                    tph ^= 1;
+                    t_issued = false;  // landed
+                }
+                for (; left > 0; --left) {
+                    if (!bar_wait(b_full + 8 * bs, bph, ab, 46)) break;
+                    if (!bar_wait(d_empty + 8 * acc, aph ^ 1, ab, 46)) break;
+                    fence_after();
+                    const uint32_t d = tmem + acc * kUnit;
+                    for (int r = 0; r < rank; r += 16) {
+                        const uint32_t chunk = r >> 6, in = (r & 63) * 2;
+                        const uint64_t hi = operand_desc(t_base + chunk * kBoxBytes + in);
+                        const uint64_t b = operand_desc(b_ring + bs * plan.b_bytes + chunk * (kUnit * 128) + in);
+                        mma_bf16(d, hi, b, idesc, r > 0 ? 1u : 0u);
+                        mma_bf16(d, hi + (plan.lo_offset >> 4), b, idesc, 1u);
+                    }
+                    mma_commit(b_empty + 8 * bs);
+                    mma_commit(d_full + 8 * acc);
                     if (++bs == plan.b_slots) {
                         bs = 0;
                         bph ^= 1;
                     }
-                }
-            }
-            if (!ok) {
-                const uint64_t deadline = timer_ns() + kTimeoutNs;
-                if (y_issued > 0 && count > 0) bar_drain(t_full, 0, deadline);
-                for (int i = 0; i < y_issued; ++i) {
-                    if (--ys < 0) {
-                        ys = plan.y_slots - 1;
-                        yph ^= 1;
-                    }
-                    bar_drain(y_full + 8 * ys, yph, deadline);
-                }
-                for (int i = 0; i < b_issued; ++i) {
-                    if (--bs < 0) {
-                        bs = plan.b_slots - 1;
-                        bph ^= 1;
-                    }
-                    bar_drain(b_full + 8 * bs, bph, deadline);
-                }
-            }
-        }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = bf16_idesc(kUnitCols);
-            int bs = 0, acc = 0;
-            uint32_t bph = 0, aph = 0;
-            int64_t total = int64_t(u1 - u0) * count;
-            if (total > 0 && !bar_wait(t_full, 0, ab, 46)) total = 0;
-            for (int64_t i = 0; i < total; ++i) {
-                if (!bar_wait(b_full + 8 * bs, bph, ab, 46)) break;
-                if (!bar_wait(d_empty + 8 * acc, aph ^ 1, ab, 46)) break;
-                fence_after();
-                const uint32_t d = tmem + acc * kUnitCols;
-                for (int r = 0; r < rank; r += 16) {
-                    const uint32_t chunk = r >> 6, in = (r & 63) * 2;
-                    const uint64_t hi = operand_desc(t_base + chunk * (kTileRows * 128) + in);
-                    const uint64_t b = operand_desc(b_ring + bs * plan.b_bytes + chunk * 8192 + in);
-                    mma_bf16(d, hi, b, idesc, r > 0 ? 1u : 0u);
-                    mma_bf16(d, hi + (plan.lo_offset >> 4), b, idesc, 1u);
-                }
-                mma_commit(b_empty + 8 * bs);
-                mma_commit(d_full + 8 * acc);
-                if (++bs == plan.b_slots) {
-                    bs = 0;
-                    bph ^= 1;
-                }
-                if (++acc == kAccs) {
-                    acc = 0;
-                    aph ^= 1;
-                }
-            }
-            mma_commit(drain);
-        }
-        __syncwarp();
-    } else {
-        const int quad = warp & 3, row = quad * 32 + lane;
-        const int mine = ts.row[row];
-        const uint32_t swz = (row & 7) << 4;
-        const bool stored = m0 + quad * 32 < p.rows;  // a box of this warp's rows
-        int ys = 0, acc = 0, prev = -1;
-        uint32_t yph = 0, aph = 0;
-        bool ok = true;
-        for (int i = 0, u = u_first; i < u1 - u0 && ok; ++i, u = u + 1 < u1 ? u + 1 : u0) {
-            if (!bar_wait_warp(y_full + 8 * ys, yph, ab, 47)) break;
-            const uint32_t y = y_ring + ys * kYBytes + row * 128;
-            for (int d = 0; d < count; ++d) {
-                if (!bar_wait_warp(d_full + 8 * acc, aph, ab, 47)) {
-                    ok = false;
-                    break;
-                }
-                fence_after();
-                const uint32_t src = tmem + acc * kUnitCols + (static_cast<uint32_t>(quad * 32) << 16);
-                uint32_t f[64];
-                __syncwarp();
-                tmem_ld64(src, f);
-                fence_before();
-                __syncwarp();
-                if (lane == 0) bar_arrive(d_empty + 8 * acc);  // read: back to the MMA thread
-                if (mine == d) {
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const uint32_t at = y + ((16 * c) ^ swz);
-                        uint4 v = ld_shared_16B(at);
-                        v.x = add_pair(v.x, f[8 * c], f[8 * c + 1]);
-                        v.y = add_pair(v.y, f[8 * c + 2], f[8 * c + 3]);
-                        v.z = add_pair(v.z, f[8 * c + 4], f[8 * c + 5]);
-                        v.w = add_pair(v.w, f[8 * c + 6], f[8 * c + 7]);
-                        st_shared_16B(at, v);
+                    if (++acc == kAccs) {
+                        acc = 0;
+                        aph ^= 1;
                     }
                 }
-                if (++acc == kAccs) {
-                    acc = 0;
-                    aph ^= 1;
-                }
             }
-            if (!ok) break;
-            // This warp's 32 rows go out; the slot of the unit before is free
-            // once its store has read it.
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) {
-                if (stored)
-                    store_2d(&maps.out, y_ring + ys * kYBytes + quad * 4096, u * kUnitCols,
-                             static_cast<int>(m0) + quad * 32);
-                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                if (prev >= 0) bar_arrive(y_empty + 8 * prev);
+        } else {
+            const int quad = warp & 3, row = quad * 32 + lane;
+            const int mine = ts.row[row];
+            const uint32_t swz = (row & 7) << 4;
+            const bool stored = m0 + quad * 32 < p.rows;  // a box of this warp's rows
+            bool ok = true;
+            for (int u = u0; u < u1; ++u) {
+                if (!bar_wait_warp(y_full + 8 * ys, yph, ab, 47)) break;
+                const uint32_t y = y_ring + ys * kYBytes + row * 128;
+                for (int d = 0; d < count; ++d) {
+                    if (!bar_wait_warp(d_full + 8 * acc, aph, ab, 47)) {
+                        ok = false;
+                        break;
+                    }
+                    fence_after();
+                    const uint32_t src = tmem + acc * kUnit + (static_cast<uint32_t>(quad * 32) << 16);
+                    const bool any = count == 1 || __any_sync(0xFFFFFFFFu, mine == d);  // rows of it
+#pragma unroll
+                    for (int h = 0; h < kUnit; h += 64) {
+                        uint32_t f[64];
+                        if (any) tmem_ld64(src + h, f);
+                        if (h + 64 == kUnit) {  // read: back to the MMA thread
+                            fence_before();
+                            __syncwarp();
+                            if (lane == 0) bar_arrive(d_empty + 8 * acc);
+                        }
+                        if (mine == d) {
+                            const uint32_t yh = y + h * (kTileRows * 2);
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                const uint32_t at = yh + ((16 * c) ^ swz);
+                                uint4 v = ld_shared_16B(at);
+                                v.x = add_pair(v.x, f[8 * c], f[8 * c + 1]);
+                                v.y = add_pair(v.y, f[8 * c + 2], f[8 * c + 3]);
+                                v.z = add_pair(v.z, f[8 * c + 4], f[8 * c + 5]);
+                                v.w = add_pair(v.w, f[8 * c + 6], f[8 * c + 7]);
+                                st_shared_16B(at, v);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (++acc == kAccs) {
+                        acc = 0;
+                        aph ^= 1;
+                    }
+                }
+                if (!ok) break;
+                // This warp's 32 rows go out; the slot of the unit before is free
+                // once its store has read it.
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+#pragma unroll
+                    for (int h = 0; h < kUnit; h += 64)
+                        if (stored && u * kUnit + h < p.n)
+                            store_2d(&maps.out, y_ring + ys * kYBytes + h * (kTileRows * 2) + quad * 4096,
+                                     u * kUnit + h, static_cast<int>(m0) + quad * 32);
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                    if (prev >= 0) bar_arrive(y_empty + 8 * prev);
+                }
+                prev = ys;
+                if (++ys == plan.y_slots) {
+                    ys = 0;
+                    yph ^= 1;
+                }
             }
-            prev = ys;
-            if (++ys == plan.y_slots) {
-                ys = 0;
+        }
+        // Every role is done with this tile (its t, its adapters), and every
+        // product of it has been read.
+        __syncthreads();
+        if (abort_flag) break;
+    }
+
+    if (warp == 0 && lane == 0 && abort_flag) {  // copies still in flight
+        const uint64_t deadline = timer_ns() + kTimeoutNs;
+        for (int i = 0; i < y_issued; ++i) {
+            if (--ys < 0) {
+                ys = plan.y_slots - 1;
                 yph ^= 1;
             }
+            bar_drain(y_full + 8 * ys, yph, deadline);
         }
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        for (int i = 0; i < b_issued; ++i) {
+            if (--bs < 0) {
+                bs = plan.b_slots - 1;
+                bph ^= 1;
+            }
+            bar_drain(b_full + 8 * bs, bph, deadline);
+        }
     }
+    if (warp >= 2 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");  // this grid never ends before the shrink
-    __syncthreads();
     if (warp == 1) {
-        if (lane == 0) bar_drain(drain, 0, timer_ns() + kTimeoutNs);  // every MMA has completed
+        if (lane == 0) {  // every MMA, and t's copies, have completed
+            const uint64_t deadline = timer_ns() + kTimeoutNs;
+            mma_commit(drain);
+            bar_drain(drain, 0, deadline);
+            if (abort_flag && t_issued) bar_drain(t_full, tph, deadline);
+        }
         __syncwarp();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                     "r"(kAccs * kUnitCols)
-                     : "memory");
     }
+    __syncthreads();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kAccCols)
+                     : "memory");
 }
 
 // ---------------------------------------------------------------- host
@@ -799,39 +877,15 @@ constexpr int kSms = 148;
 
 int64_t row_tiles(int64_t rows) { return (rows + kTileRows - 1) / kTileRows; }
 
-// CTAs of a shrink cluster: of 1, 2, 4 and 8, the number that leaves the SM
-// with the most CTAs the least of K to read, at least 4 blocks of 64 each; of
-// equals the largest that still runs at once, two CTAs per SM keeping more
-// bytes in flight than one.
+// CTAs of a shrink cluster: the largest of 1, 2, 4 and 8 that leaves the grid
+// within one CTA per SM and each CTA at least 4 blocks of 64. (Clusters of 8
+// with two CTAs per SM did not all fit at once, and the last ones doubled the
+// time.)
 int shrink_splits(int64_t rows, int64_t k) {
     const int64_t tiles = row_tiles(rows), blocks = (k + 63) / 64;
-    int best = 1;
-    int64_t best_cost = INT64_MAX;
-    for (int s = 1; s <= kMaxSplits && (s == 1 || blocks / s >= 4); s *= 2) {
-        const int64_t cost = (tiles * s + kSms - 1) / kSms * ((blocks + s - 1) / s);
-        if (cost < best_cost || (cost == best_cost && tiles * s <= 2 * kSms)) {
-            best = s;
-            best_cost = cost;
-        }
-    }
-    return best;
-}
-
-// Column ranges of the expand: the number whose last wave of CTAs wastes
-// least, each range costing about three units of its own to start.
-int expand_ranges(int64_t rows, int64_t n, int64_t rank) {
-    const int64_t tiles = row_tiles(rows), units = (n + kUnitCols - 1) / kUnitCols;
-    const int64_t at_once = rank <= 64 ? 2 * kSms : kSms;
-    int best = 1;
-    int64_t best_cost = INT64_MAX;
-    for (int64_t r = 1; r <= units && r <= 2 * at_once / tiles + 4; ++r) {
-        const int64_t cost = (tiles * r + at_once - 1) / at_once * ((units + r - 1) / r + 3);
-        if (cost < best_cost) {
-            best = static_cast<int>(r);
-            best_cost = cost;
-        }
-    }
-    return best;
+    int s = 1;
+    while (2 * s <= kMaxSplits && tiles * 2 * s <= kSms && blocks / (2 * s) >= 4) s *= 2;
+    return s;
 }
 
 template <class K>
@@ -840,24 +894,45 @@ cudaError_t allow_smem(K kernel, uint32_t bytes) {
                                 static_cast<int>(bytes));
 }
 
-template <int NB>
 cudaError_t launch_shrink(const ShrinkMaps &maps, const nvfp4_lora_args &p, int splits, float *partial,
                           uint16_t *t, int *err, cudaStream_t stream) {
-    using Cfg = ShrinkConfig<NB>;
-    cudaError_t e = allow_smem(lora_shrink_kernel<NB>, Cfg::SMEM_BYTES);
+    const int64_t grid = row_tiles(p.rows) * splits;
+    const uint32_t ring = splits == 1 && grid <= kSms ? kLargeRing : kSmallRing;
+    const cudaError_t e = allow_smem(lora_shrink_kernel, kLargeRing + 1024);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = static_cast<unsigned>(splits);
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(row_tiles(p.rows) * splits));
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
+    cfg.dynamicSmemBytes = ring + 1024;
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, lora_shrink_kernel<NB>, maps, p, splits, partial, t, err);
+    return cudaLaunchKernelEx(&cfg, lora_shrink_kernel, maps, p, splits, ring, partial, t, err);
+}
+
+template <int kUnit>
+cudaError_t launch_expand(const ExpandMaps &maps, const nvfp4_lora_args &p, const ExpandPlan &plan,
+                          int64_t at_once, int *err, cudaStream_t stream) {
+    const cudaError_t e = allow_smem(lora_expand_kernel<kUnit>, plan.smem_bytes);
+    if (e != cudaSuccess) return e;
+    const int64_t units = row_tiles(p.rows) * ((p.n + kUnit - 1) / kUnit);
+    const int64_t chunks = units / kUnitsPerCta;
+    const int64_t grid = units < at_once ? units : chunks > at_once ? chunks : at_once;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = plan.smem_bytes;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, lora_expand_kernel<kUnit>, maps, p, plan, err);
 }
 
 size_t partial_bytes(int64_t rows, int64_t rank, int splits) {
@@ -880,6 +955,7 @@ cudaError_t launch_lora_tile(const nvfp4_lora_args &p, cudaStream_t stream) {
     float *partial = static_cast<float *>(p.workspace);
     uint16_t *t = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(p.workspace) +
                                                partial_bytes(p.rows, p.rank, splits));
+    const ExpandPlan plan = expand_plan(p.rank);
     ShrinkMaps sm;
     ExpandMaps em;
     std::memset(&sm, 0, sizeof(sm));
@@ -887,28 +963,14 @@ cudaError_t launch_lora_tile(const nvfp4_lora_args &p, cudaStream_t stream) {
     if (!encode_map(&sm.x, p.x, p.k, p.rows, p.x_stride, kTileRows) ||
         !encode_map(&sm.a, p.a, p.k, p.slots * p.rank, p.k, static_cast<uint32_t>(p.rank)) ||
         !encode_map(&em.y, p.y, p.n, p.rows, p.y_stride, kTileRows) ||
-        !encode_map(&em.b, p.b, p.rank, p.slots * p.n, p.rank, kUnitCols) ||
+        !encode_map(&em.b, p.b, p.rank, p.slots * p.n, p.rank, static_cast<uint32_t>(expand_unit(p.rank))) ||
         !encode_map(&em.out, p.out, p.n, p.rows, p.out_stride, 32) ||
         !encode_map(&em.t, t, tl.groups * 64, p.rows, tl.groups * 64, kTileRows))
         return cudaErrorInvalidValue;
-    cudaError_t e = p.rank <= 64 ? launch_shrink<64>(sm, p, splits, partial, t, err, stream)
-                                 : launch_shrink<128>(sm, p, splits, partial, t, err, stream);
+    cudaError_t e = launch_shrink(sm, p, splits, partial, t, err, stream);
     if (e != cudaSuccess) return e;
-    const ExpandPlan plan = expand_plan(p.rank);
-    e = allow_smem(lora_expand_kernel, plan.smem_bytes);
-    if (e != cudaSuccess) return e;
-    const int ranges = expand_ranges(p.rows, p.n, p.rank);
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(row_tiles(p.rows) * ranges));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = plan.smem_bytes;
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, lora_expand_kernel, em, p, plan, ranges, err);
+    return expand_unit(p.rank) == 64 ? launch_expand<64>(em, p, plan, 2 * kSms, err, stream)
+                                     : launch_expand<128>(em, p, plan, kSms, err, stream);
 }
 
 }  // namespace nvfp4
