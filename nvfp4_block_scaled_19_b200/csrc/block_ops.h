@@ -21,7 +21,7 @@ size_t lora_workspace_bytes(int64_t rows, int64_t k, int64_t n, int64_t rank);
 cudaError_t launch_lora(const nvfp4_lora_args &p, cudaStream_t stream);
 
 // The same for many rows, on 128-row tensor-core tiles (lora_tile.cu).
-size_t lora_tile_workspace_bytes(int64_t rows, int64_t k, int64_t rank);
+size_t lora_tile_workspace_bytes(int64_t rows, int64_t rank);
 cudaError_t launch_lora_tile(const nvfp4_lora_args &p, cudaStream_t stream);
 
 }  // namespace nvfp4

@@ -211,8 +211,9 @@ cudaError_t launch_rows(const nvfp4_lora_args &p, cudaStream_t stream) {
 constexpr int64_t kTileFromRows = 97;
 
 size_t lora_workspace_bytes(int64_t rows, int64_t k, int64_t n, int64_t rank) {
+    (void)k;
     (void)n;
-    return rows < kTileFromRows ? 0 : lora_tile_workspace_bytes(rows, k, rank);
+    return rows < kTileFromRows ? 0 : lora_tile_workspace_bytes(rows, rank);
 }
 
 cudaError_t launch_lora(const nvfp4_lora_args &p, cudaStream_t stream) {

@@ -27,8 +27,8 @@
 // of x, above what the register-operand MMAs sustain beside the loads and far
 // below tcgen05's rate.
 //
-// Roles of both: warp 0 TMA producer, warp 1 MMA issuer (and tensor memory),
-// warps 2-5 epilogue (one 32-lane quadrant each).  Every wait is bounded; on a
+// Roles of both: warp 0 TMA producer, warp 1 MMA issuer, warps 2-5 epilogue (one
+// 32-lane quadrant each); in the shrink warp 6 is a second producer.  Every wait is bounded; on a
 // timeout the kernel records NVFP4_ERR_TIMEOUT (tags 40-47), all roles stop,
 // copies and MMAs in flight are drained with bounded waits and tensor memory is
 // freed.
@@ -137,12 +137,6 @@ __device__ __forceinline__ void load_2d(const CUtensorMap *m, uint32_t bar, uint
         : "memory");
 }
 
-__device__ __forceinline__ void prefetch_2d(const CUtensorMap *m, int x, int y) {
-    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(m), "r"(x),
-                 "r"(y)
-                 : "memory");
-}
-
 __device__ __forceinline__ void store_2d(const CUtensorMap *m, uint32_t src, int x, int y) {
     asm volatile(
         "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(m),
@@ -186,20 +180,28 @@ __device__ __forceinline__ void fence_after() {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
-// 16 columns of this warp's 32 lanes, complete on return.
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&f)[16]) {
-    uint32_t r[16];
+template <int k>
+__device__ __forceinline__ void tmem_ld16_part(uint32_t addr, uint32_t (&r)[64]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32"
-        " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(addr)
+        " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[k]), "=r"(r[k + 1]), "=r"(r[k + 2]), "=r"(r[k + 3]), "=r"(r[k + 4]), "=r"(r[k + 5]),
+          "=r"(r[k + 6]), "=r"(r[k + 7]), "=r"(r[k + 8]), "=r"(r[k + 9]), "=r"(r[k + 10]),
+          "=r"(r[k + 11]), "=r"(r[k + 12]), "=r"(r[k + 13]), "=r"(r[k + 14]), "=r"(r[k + 15])
+        : "r"(addr + k)
         : "memory");
+}
+
+// The first min(n16, 4) x 16 columns of this warp's 32 lanes, complete on return.
+__device__ __forceinline__ void tmem_ld_up_to_64(uint32_t addr, uint32_t (&r)[64], int n16) {
+    tmem_ld16_part<0>(addr, r);
+    if (n16 > 1) tmem_ld16_part<16>(addr, r);
+    if (n16 > 2) tmem_ld16_part<32>(addr, r);
+    if (n16 > 3) tmem_ld16_part<48>(addr, r);
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    // No use of the values moves above the wait.
 #pragma unroll
-    for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(r[i]);
+    for (int i = 0; i < 64; ++i) asm volatile("" : "+r"(r[i]));
 }
 
 // 64 columns of this warp's 32 lanes, complete on return.
@@ -333,26 +335,31 @@ struct alignas(64) ExpandMaps {
 
 // ---------------------------------------------------------------- shrink
 
-constexpr int kMaxStages = 8;
 constexpr int kAccCols = 256;  // tensor memory of a CTA of either kernel: two fit an SM
 
-// Rings of 96 KB (two CTAs per SM) or 192 KB (one, where the grid has no more
-// and no clusters: those do not fill every SM), cut into stages of the tile's own size: x's piece and those of the adapters of
-// a pass.
-constexpr uint32_t kSmallRing = 96 * 1024, kLargeRing = 192 * 1024;
+// Two rings, of x's 128 x 64 pieces and of the adapters' pieces of a pass, with
+// as many slots as fit for the tile's adapters.  What bounds the stream of x is
+// bytes in flight: a box of 128 rows takes about 2 us from HBM, so 96 KB of x in
+// flight are worth 48 GB/s of an SM.  192 KB where a CTA has its SM alone, else
+// 96 KB and two CTAs per SM.
+constexpr uint32_t kLargeRings = 192 * 1024, kSmallRings = 96 * 1024;
+constexpr int kMaxSlots = 8;
+constexpr int kShrinkThreads = kThreads + 32;  // warp 6 loads the adapters
 
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kShrinkThreads)
     lora_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const nvfp4_lora_args p,
                        const int splits, const uint32_t ring_bytes, float *partial, uint16_t *t,
                        int *err) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ TileSlots ts;
-    __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 3];
+    __shared__ float scales[kTileRows];
+    __shared__ __align__(8) uint64_t bars[4 * kMaxSlots + 3];
     __shared__ uint32_t tmem_holder;
     __shared__ int abort_flag;
-    const uint32_t ring = (s32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t full = s32(bars), empty = full + 8 * kMaxStages;
-    const uint32_t acc_full = empty + 8 * kMaxStages, acc_empty = acc_full + 8, drain = acc_empty + 8;
+    const uint32_t x_ring = (s32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t x_full = s32(bars), x_empty = x_full + 8 * kMaxSlots;
+    const uint32_t a_full = x_empty + 8 * kMaxSlots, a_empty = a_full + 8 * kMaxSlots;
+    const uint32_t acc_full = a_empty + 8 * kMaxSlots, acc_empty = acc_full + 8, drain = acc_empty + 8;
     const Abort ab{&abort_flag, err};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tile = blockIdx.x / splits, split = blockIdx.x % splits;
@@ -360,63 +367,98 @@ __global__ void __launch_bounds__(kThreads)
     const int rank = static_cast<int>(p.rank);
     const int k_blocks = static_cast<int>((p.k + 63) / 64);
     const int kb0 = static_cast<int>(int64_t(k_blocks) * split / splits);
-    const int kb1 = static_cast<int>(int64_t(k_blocks) * (split + 1) / splits);
+    const int kbs = static_cast<int>(int64_t(k_blocks) * (split + 1) / splits) - kb0;
+    // Pieces of x asked for before the tile's adapters are known: the slots that
+    // there are with the most adapters of a pass (32 KB a slot).
+    const int early = min(static_cast<int>(ring_bytes / (kXBytes + 32 * 1024)), kbs);
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kMaxStages; ++s) {
-            bar_init(full + 8 * s, 1);
-            bar_init(empty + 8 * s, 1);
+        for (int s = 0; s < kMaxSlots; ++s) {
+            bar_init(x_full + 8 * s, 1);
+            bar_init(x_empty + 8 * s, 1);
+            bar_init(a_full + 8 * s, 1);
+            bar_init(a_empty + 8 * s, 1);
         }
         bar_init(acc_full, 1);
         bar_init(acc_empty, 4);
         bar_init(drain, 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        for (int i = 0; i < early; ++i) {
+            bar_expect(x_full + 8 * i, kXBytes);
+            load_2d(&maps.x, x_full + 8 * i, x_ring + i * kXBytes, (kb0 + i) * 64, static_cast<int>(m0));
+        }
     }
-    if (threadIdx.x == 32)  // the first of x on its way while the adapters are found
-        for (int kb = kb0; kb < min(kb0 + 4, kb1); ++kb)
-            prefetch_2d(&maps.x, kb * 64, static_cast<int>(m0));
-    find_slots(ts, p, m0);
-    if (ts.count == 0) return;  // no row has an adapter (the same in the whole cluster)
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          s32(&tmem_holder)),
                      "r"(kAccCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        fence_before();
     }
-    fence_before();
-    __syncthreads();
+    find_slots(ts, p, m0);
     fence_after();
-    const uint32_t tmem = tmem_holder;
     // The expand may start its prologue once every CTA here holds its tensor memory.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int group = min(kAccCols / rank, ts.count);  // adapters per pass over x
-    const int passes = (ts.count + group - 1) / group;
-    const uint32_t stage_bytes = kXBytes + group * rank * 128;  // at most 48 KB
-    const int stages = min(kMaxStages, static_cast<int>(ring_bytes / stage_bytes));
+    const uint32_t tmem = tmem_holder;
+    const int count = ts.count;
+    const int group = max(1, min(kAccCols / rank, count));  // adapters per pass over x
+    const int passes = (count + group - 1) / group;          // 0: no row has an adapter
+    const uint32_t a_slot = group * rank * 128;              // at most 32 KB
+    const int slots = min(kMaxSlots, static_cast<int>(ring_bytes / (kXBytes + a_slot)));
+    const uint32_t a_ring = x_ring + slots * kXBytes;
+    const int steps = passes * kbs;
 
     if (warp == 0) {
         if (lane == 0) {
-            int stage = 0, issued = 0;
+            int slot = early % slots, issued = early;
+            uint32_t phase = early == slots ? 1 : 0;
+            bool ok = passes > 0;
+            for (int i = early; i < steps && ok; ++i) {
+                if (!bar_wait(x_empty + 8 * slot, phase ^ 1, ab, 40)) {
+                    ok = false;
+                    break;
+                }
+                bar_expect(x_full + 8 * slot, kXBytes);
+                load_2d(&maps.x, x_full + 8 * slot, x_ring + slot * kXBytes, (kb0 + i % kbs) * 64,
+                        static_cast<int>(m0));
+                if (issued < slots) ++issued;
+                if (++slot == slots) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            }
+            if (!ok) {  // given up, or nothing to multiply: the copies in flight land first
+                const uint64_t deadline = timer_ns() + kTimeoutNs;
+                for (int i = 0; i < issued; ++i) {
+                    if (--slot < 0) {
+                        slot = slots - 1;
+                        phase ^= 1;
+                    }
+                    bar_drain(x_full + 8 * slot, phase, deadline);
+                }
+            }
+        }
+    } else if (warp == 6) {
+        if (lane == 0) {
+            int slot = 0, issued = 0;
             uint32_t phase = 0;
             bool ok = true;
             for (int q = 0; q < passes && ok; ++q) {
-                const int d0 = q * group, d1 = min(ts.count, d0 + group);
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!bar_wait(empty + 8 * stage, phase ^ 1, ab, 40)) {
+                const int d0 = q * group, d1 = min(count, d0 + group);
+                for (int kb = kb0; kb < kb0 + kbs; ++kb) {
+                    if (!bar_wait(a_empty + 8 * slot, phase ^ 1, ab, 40)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t dst = ring + stage * stage_bytes, bar = full + 8 * stage;
-                    bar_expect(bar, kXBytes + (d1 - d0) * rank * 128);
-                    load_2d(&maps.x, bar, dst, kb * 64, static_cast<int>(m0));
+                    bar_expect(a_full + 8 * slot, (d1 - d0) * rank * 128);
                     for (int d = d0; d < d1; ++d)
-                        load_2d(&maps.a, bar, dst + kXBytes + (d - d0) * rank * 128, kb * 64,
-                                ts.list[d] * rank);
-                    if (issued < stages) ++issued;
-                    if (++stage == stages) {
-                        stage = 0;
+                        load_2d(&maps.a, a_full + 8 * slot, a_ring + slot * a_slot + (d - d0) * rank * 128,
+                                kb * 64, ts.list[d] * rank);
+                    if (issued < slots) ++issued;
+                    if (++slot == slots) {
+                        slot = 0;
                         phase ^= 1;
                     }
                 }
@@ -424,41 +466,40 @@ __global__ void __launch_bounds__(kThreads)
             if (!ok) {
                 const uint64_t deadline = timer_ns() + kTimeoutNs;
                 for (int i = 0; i < issued; ++i) {
-                    if (--stage < 0) {
-                        stage = stages - 1;
+                    if (--slot < 0) {
+                        slot = slots - 1;
                         phase ^= 1;
                     }
-                    bar_drain(full + 8 * stage, phase, deadline);
+                    bar_drain(a_full + 8 * slot, phase, deadline);
                 }
             }
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            int stage = 0;
+            int slot = 0;
             uint32_t phase = 0;
             bool ok = true;
             for (int q = 0; q < passes && ok; ++q) {
-                const int d0 = q * group, d1 = min(ts.count, d0 + group);
+                const int d0 = q * group, d1 = min(count, d0 + group);
                 const uint32_t idesc = bf16_idesc((d1 - d0) * rank);
-                if (!bar_wait(acc_empty, (q & 1) ^ 1, ab, 41)) {
-                    ok = false;
-                    break;
-                }
+                if (!bar_wait(acc_empty, (q & 1) ^ 1, ab, 41)) break;
                 fence_after();
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!bar_wait(full + 8 * stage, phase, ab, 42)) {
+                for (int kb = 0; kb < kbs; ++kb) {
+                    if (!bar_wait(a_full + 8 * slot, phase, ab, 42) ||
+                        !bar_wait(x_full + 8 * slot, phase, ab, 42)) {
                         ok = false;
                         break;
                     }
                     fence_after();
-                    const uint64_t a = operand_desc(ring + stage * stage_bytes);
-                    const uint64_t b = operand_desc(ring + stage * stage_bytes + kXBytes);
+                    const uint64_t a = operand_desc(x_ring + slot * kXBytes);
+                    const uint64_t b = operand_desc(a_ring + slot * a_slot);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        mma_bf16(tmem, a + 2 * j, b + 2 * j, idesc, (kb > kb0 || j > 0) ? 1u : 0u);
-                    mma_commit(empty + 8 * stage);
-                    if (++stage == stages) {
-                        stage = 0;
+                        mma_bf16(tmem, a + 2 * j, b + 2 * j, idesc, (kb > 0 || j > 0) ? 1u : 0u);
+                    mma_commit(x_empty + 8 * slot);
+                    mma_commit(a_empty + 8 * slot);
+                    if (++slot == slots) {
+                        slot = 0;
                         phase ^= 1;
                     }
                 }
@@ -473,95 +514,105 @@ __global__ void __launch_bounds__(kThreads)
         const TLayout tl(rank);
         float *dst = partial + (int64_t(split) * p.rows + m0 + row) * rank;
         uint16_t *tdst = t + (m0 + row) * (tl.groups * 64);
+        if (row < count) scales[row] = __ldg(p.scale + ts.list[row]);
         const float c = mine >= 0 ? __ldg(p.scale + ts.list[mine]) : 0.0f;
         for (int q = 0; q < passes; ++q) {
-            const int d0 = q * group, d1 = min(ts.count, d0 + group);
+            const int d0 = q * group, d1 = min(count, d0 + group);
             if (!bar_wait_warp(acc_full, q & 1, ab, 43)) break;
             fence_after();
             const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-            for (int d = d0; d < d1; ++d)
-                for (int r = 0; r < rank; r += 16) {
-                    float f[16];
-                    __syncwarp();
-                    tmem_ld16(acc + (d - d0) * rank + r, f);
-                    if (mine != d) continue;  // also rows past the last one
-                    if (splits == 1) {
+            for (int d = d0; d < d1; ++d) {
+                if (!__any_sync(0xFFFFFFFFu, mine == d)) continue;  // none of this warp's rows
+                for (int r0 = 0; r0 < rank; r0 += 64) {
+                    uint32_t f[64];
+                    tmem_ld_up_to_64(acc + (d - d0) * rank + r0, f, (rank - r0) >> 4);
+                    if (mine == d) {  // never a row past the last one
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) f[j] *= c;
-                        store_t8(f, tdst + r, tdst + tl.lo_at + r);
-                        store_t8(f + 8, tdst + r + 8, tdst + tl.lo_at + r + 8);
-                    } else if (passes == 1) {  // the ring is free: every stage has been multiplied
+                        for (int h = 0; h < 64; h += 8) {
+                            const int r = r0 + h;
+                            if (r >= rank) break;
+                            if (splits == 1) {
+                                float v[8];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            st_shared_16B(ring + (((r >> 2) + j) * kTileRows + row) * 16,
-                                          make_uint4(__float_as_uint(f[4 * j]), __float_as_uint(f[4 * j + 1]),
-                                                     __float_as_uint(f[4 * j + 2]), __float_as_uint(f[4 * j + 3])));
-                    } else {
-                        float4 *o = reinterpret_cast<float4 *>(dst + r);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            o[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+                                for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(f[h + j]) * c;
+                                store_t8(v, tdst + r, tdst + tl.lo_at + r);
+                            } else if (passes == 1) {  // x's ring is free: all of it has been multiplied
+                                const uint32_t at = x_ring + ((r >> 2) * kTileRows + row) * 16;
+                                st_shared_16B(at, make_uint4(f[h], f[h + 1], f[h + 2], f[h + 3]));
+                                st_shared_16B(at + kTileRows * 16,
+                                              make_uint4(f[h + 4], f[h + 5], f[h + 6], f[h + 7]));
+                            } else {
+                                uint4 *o = reinterpret_cast<uint4 *>(dst + r);
+                                o[0] = make_uint4(f[h], f[h + 1], f[h + 2], f[h + 3]);
+                                o[1] = make_uint4(f[h + 4], f[h + 5], f[h + 6], f[h + 7]);
+                            }
+                        }
                     }
+                    __syncwarp();
                 }
+            }
             fence_before();
             __syncwarp();
             if (lane == 0) bar_arrive(acc_empty);
         }
     }
-    __syncthreads();
+    if (splits == 1) {
+        __syncthreads();
+    } else {
+        // Every split's sums are written: this CTA's share of the rows, eight
+        // ranks per thread at a time, in the order of the splits.
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                         : "memory");
+        const TLayout tl(rank);
+        const int share = (kTileRows + splits - 1) / splits;
+        for (int i = threadIdx.x; i < share * (rank >> 3); i += kShrinkThreads) {
+            const int row = split * share + i % share, r = i / share * 8;
+            const int d = row < kTileRows ? ts.row[row] : -1;
+            if (d < 0) continue;
+            float4 w[kMaxSplits][2];  // asked for together
+            if (passes == 1) {
+                const uint32_t at = x_ring + ((r >> 2) * kTileRows + row) * 16;
+#pragma unroll
+                for (int s = 0; s < kMaxSplits; ++s)
+                    if (s < splits) {
+                        w[s][0] = ld_cluster_16B(at, s);
+                        w[s][1] = ld_cluster_16B(at + kTileRows * 16, s);
+                    }
+            } else {
+                const float *src = partial + (m0 + row) * rank + r;
+#pragma unroll
+                for (int s = 0; s < kMaxSplits; ++s)
+                    if (s < splits) {
+                        const float4 *o = reinterpret_cast<const float4 *>(src + s * p.rows * rank);
+                        w[s][0] = o[0];
+                        w[s][1] = o[1];
+                    }
+            }
+            float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int s = 0; s < kMaxSplits; ++s)
+                if (s < splits) {
+                    v[0] += w[s][0].x; v[1] += w[s][0].y; v[2] += w[s][0].z; v[3] += w[s][0].w;
+                    v[4] += w[s][1].x; v[5] += w[s][1].y; v[6] += w[s][1].z; v[7] += w[s][1].w;
+                }
+            const float c = scales[d];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] *= c;
+            uint16_t *o = t + (m0 + row) * (tl.groups * 64) + r;
+            store_t8(v, o, o + tl.lo_at);
+        }
+        // No CTA of the cluster leaves while another reads its shared memory.
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                         : "memory");
+    }
     if (warp == 1) {
         if (lane == 0) bar_drain(drain, 0, timer_ns() + kTimeoutNs);  // every MMA has completed
         __syncwarp();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                     "r"(kAccCols)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kAccCols)
                      : "memory");
     }
-    if (splits == 1) return;
-    // Every split's sums are written: this CTA's share of the rows, eight ranks
-    // per thread at a time, in the order of the splits.
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                     : "memory");
-    const TLayout tl(rank);
-    const int share = kTileRows / splits;
-    for (int i = threadIdx.x; i < share * (rank >> 3); i += kThreads) {
-        const int row = split * share + i % share, r = i / share * 8;
-        const int d = ts.row[row];
-        if (d < 0) continue;
-        float4 w[kMaxSplits][2];  // asked for together
-        if (passes == 1) {
-            const uint32_t at = ring + ((r >> 2) * kTileRows + row) * 16;
-#pragma unroll
-            for (int s = 0; s < kMaxSplits; ++s)
-                if (s < splits) {
-                    w[s][0] = ld_cluster_16B(at, s);
-                    w[s][1] = ld_cluster_16B(at + kTileRows * 16, s);
-                }
-        } else {
-            const float *src = partial + (m0 + row) * rank + r;
-#pragma unroll
-            for (int s = 0; s < kMaxSplits; ++s)
-                if (s < splits) {
-                    const float4 *o = reinterpret_cast<const float4 *>(src + s * p.rows * rank);
-                    w[s][0] = o[0];
-                    w[s][1] = o[1];
-                }
-        }
-        float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int s = 0; s < kMaxSplits; ++s)
-            if (s < splits) {
-                v[0] += w[s][0].x; v[1] += w[s][0].y; v[2] += w[s][0].z; v[3] += w[s][0].w;
-                v[4] += w[s][1].x; v[5] += w[s][1].y; v[6] += w[s][1].z; v[7] += w[s][1].w;
-            }
-        const float c = __ldg(p.scale + ts.list[d]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= c;
-        uint16_t *o = t + (m0 + row) * (tl.groups * 64) + r;
-        store_t8(v, o, o + tl.lo_at);
-    }
-    // No CTA of the cluster leaves while another reads its shared memory.
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                     : "memory");
 }
 
 // ---------------------------------------------------------------- expand
@@ -877,41 +928,57 @@ constexpr int kSms = 148;
 
 int64_t row_tiles(int64_t rows) { return (rows + kTileRows - 1) / kTileRows; }
 
-// CTAs of a shrink cluster: the largest of 1, 2, 4 and 8 that leaves the grid
-// within one CTA per SM and each CTA at least 4 blocks of 64. (Clusters of 8
-// with two CTAs per SM did not all fit at once, and the last ones doubled the
-// time.)
-int shrink_splits(int64_t rows, int64_t k) {
-    const int64_t tiles = row_tiles(rows), blocks = (k + 63) / 64;
-    int s = 1;
-    while (2 * s <= kMaxSplits && tiles * 2 * s <= kSms && blocks / (2 * s) >= 4) s *= 2;
-    return s;
-}
-
 template <class K>
 cudaError_t allow_smem(K kernel, uint32_t bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(bytes));
 }
 
-cudaError_t launch_shrink(const ShrinkMaps &maps, const nvfp4_lora_args &p, int splits, float *partial,
-                          uint16_t *t, int *err, cudaStream_t stream) {
-    const int64_t grid = row_tiles(p.rows) * splits;
-    const uint32_t ring = splits == 1 && grid <= kSms ? kLargeRing : kSmallRing;
-    const cudaError_t e = allow_smem(lora_shrink_kernel, kLargeRing + 1024);
-    if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = static_cast<unsigned>(splits);
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+cudaLaunchConfig_t shrink_config(int64_t tiles, int splits, uint32_t rings, cudaLaunchAttribute *attr,
+                                 cudaStream_t stream) {
+    attr->id = cudaLaunchAttributeClusterDimension;
+    attr->val.clusterDim.x = static_cast<unsigned>(splits);
+    attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = ring + 1024;
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits));
+    cfg.blockDim = dim3(kShrinkThreads);
+    cfg.dynamicSmemBytes = rings + 1024;
     cfg.stream = stream;
-    cfg.attrs = &attr;
+    cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, lora_shrink_kernel, maps, p, splits, ring, partial, t, err);
+    return cfg;
+}
+
+// How many clusters of `splits` CTAs run at once on the current device, one CTA
+// per SM.  (Not the SMs divided by the size: a cluster stays inside a group of
+// SMs, so larger ones leave some idle.)  Asked once; atomic, as host threads may
+// make their first calls at the same time.
+int clusters_at_once(int splits) {
+    static std::atomic<int> known[64][kMaxSplits + 1];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int n = known[dev][splits].load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaLaunchAttribute attr;
+        const cudaLaunchConfig_t cfg = shrink_config(1, splits, kLargeRings, &attr, nullptr);
+        if (cudaOccupancyMaxActiveClusters(&n, lora_shrink_kernel, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+        }
+        known[dev][splits].store(n > 0 ? n : -1, std::memory_order_relaxed);
+    }
+    return n > 0 ? n : 0;
+}
+
+// CTAs of a shrink cluster: the most of which every row tile's cluster runs at
+// once with one CTA per SM, and each has 4 blocks of 64 at least.  (Of 36
+// clusters of 4 the last waited for the first to end, which doubled the time.)
+int shrink_splits(int64_t rows, int64_t k) {
+    const int64_t tiles = row_tiles(rows), blocks = (k + 63) / 64;
+    if (2 * tiles > kSms) return 1;
+    for (int s = kMaxSplits; s > 1; --s)
+        if (blocks / s >= 4 && tiles * s <= kSms && tiles <= clusters_at_once(s)) return s;
+    return 1;
 }
 
 template <int kUnit>
@@ -935,26 +1002,28 @@ cudaError_t launch_expand(const ExpandMaps &maps, const nvfp4_lora_args &p, cons
     return cudaLaunchKernelEx(&cfg, lora_expand_kernel<kUnit>, maps, p, plan, err);
 }
 
-size_t partial_bytes(int64_t rows, int64_t rank, int splits) {
-    return splits == 1 ? 0 : static_cast<size_t>(splits) * static_cast<size_t>(rows * rank) * sizeof(float);
+// Room for every split's fp32 sums: splits times the row tiles are at most an SM
+// each, whatever the device makes of the split.
+size_t partial_bytes(int64_t rows, int64_t rank) {
+    const int64_t tiles = row_tiles(rows), most = kMaxSplits < kSms / tiles ? kMaxSplits : kSms / tiles;
+    return most <= 1 ? 0 : static_cast<size_t>(most * rows * rank) * sizeof(float);
 }
 
 }  // namespace
 
-size_t lora_tile_workspace_bytes(int64_t rows, int64_t k, int64_t rank) {
+size_t lora_tile_workspace_bytes(int64_t rows, int64_t rank) {
     const TLayout tl(static_cast<int>(rank));
-    return partial_bytes(rows, rank, shrink_splits(rows, k)) +
+    return partial_bytes(rows, rank) +
            static_cast<size_t>(rows) * static_cast<size_t>(tl.groups) * 128;
 }
 
 cudaError_t launch_lora_tile(const nvfp4_lora_args &p, cudaStream_t stream) {
     int *err = device_error_word();
     if (err == nullptr) return cudaErrorUnknown;
-    const int splits = shrink_splits(p.rows, p.k);
     const TLayout tl(static_cast<int>(p.rank));
     float *partial = static_cast<float *>(p.workspace);
     uint16_t *t = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(p.workspace) +
-                                               partial_bytes(p.rows, p.rank, splits));
+                                               partial_bytes(p.rows, p.rank));
     const ExpandPlan plan = expand_plan(p.rank);
     ShrinkMaps sm;
     ExpandMaps em;
@@ -967,7 +1036,14 @@ cudaError_t launch_lora_tile(const nvfp4_lora_args &p, cudaStream_t stream) {
         !encode_map(&em.out, p.out, p.n, p.rows, p.out_stride, 32) ||
         !encode_map(&em.t, t, tl.groups * 64, p.rows, tl.groups * 64, kTileRows))
         return cudaErrorInvalidValue;
-    cudaError_t e = launch_shrink(sm, p, splits, partial, t, err, stream);
+    cudaError_t e = allow_smem(lora_shrink_kernel, kLargeRings + 1024);
+    if (e != cudaSuccess) return e;
+    const int splits = shrink_splits(p.rows, p.k);
+    const int64_t tiles = row_tiles(p.rows);
+    const uint32_t rings = tiles * splits <= kSms ? kLargeRings : kSmallRings;
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = shrink_config(tiles, splits, rings, &attr, stream);
+    e = cudaLaunchKernelEx(&cfg, lora_shrink_kernel, sm, p, splits, rings, partial, t, err);
     if (e != cudaSuccess) return e;
     return expand_unit(p.rank) == 64 ? launch_expand<64>(em, p, plan, 2 * kSms, err, stream)
                                      : launch_expand<128>(em, p, plan, kSms, err, stream);
