@@ -27,8 +27,10 @@
 // of x, above what the register-operand MMAs sustain beside the loads and far
 // below tcgen05's rate.
 //
-// Roles of both: warp 0 TMA producer, warp 1 MMA issuer, warps 2-5 epilogue (one
-// 32-lane quadrant each); in the shrink warp 6 is a second producer.  Every wait is bounded; on a
+// Roles of both: the first and last warp TMA producers (x or y; the adapters:
+// a copy costs the thread that issues it a few hundred cycles), warp 1 MMA
+// issuer, the warps between epilogue (one 32-lane quadrant each, four for every
+// 64 columns).  Every wait is bounded; on a
 // timeout the kernel records NVFP4_ERR_TIMEOUT (tags 40-47), all roles stop,
 // copies and MMAs in flight are drained with bounded waits and tensor memory is
 // freed.
@@ -49,7 +51,7 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kTileRows = 128;
-constexpr int kThreads = 192;
+constexpr int kThreads = 224;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr uint32_t kXBytes = kTileRows * 128;  // 128 rows x 64 bf16
 constexpr int kMaxSplits = 8;  // CTAs of a shrink cluster, over K
@@ -135,6 +137,12 @@ __device__ __forceinline__ void load_2d(const CUtensorMap *m, uint32_t bar, uint
         " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
         "l"(m), "r"(bar), "r"(x), "r"(y)
         : "memory");
+}
+
+__device__ __forceinline__ void prefetch_2d(const CUtensorMap *m, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(m), "r"(x),
+                 "r"(y)
+                 : "memory");
 }
 
 __device__ __forceinline__ void store_2d(const CUtensorMap *m, uint32_t src, int x, int y) {
@@ -344,22 +352,20 @@ constexpr int kAccCols = 256;  // tensor memory of a CTA of either kernel: two f
 // 96 KB and two CTAs per SM.
 constexpr uint32_t kLargeRings = 192 * 1024, kSmallRings = 96 * 1024;
 constexpr int kMaxSlots = 8;
-constexpr int kShrinkThreads = kThreads + 32;  // warp 6 loads the adapters
 
-__global__ void __launch_bounds__(kShrinkThreads)
+__global__ void __launch_bounds__(kThreads)
     lora_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const nvfp4_lora_args p,
                        const int splits, const uint32_t ring_bytes, float *partial, uint16_t *t,
                        int *err) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ TileSlots ts;
     __shared__ float scales[kTileRows];
-    __shared__ __align__(8) uint64_t bars[4 * kMaxSlots + 3];
+    __shared__ __align__(8) uint64_t bars[2 * kMaxSlots + 3];
     __shared__ uint32_t tmem_holder;
     __shared__ int abort_flag;
     const uint32_t x_ring = (s32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t x_full = s32(bars), x_empty = x_full + 8 * kMaxSlots;
-    const uint32_t a_full = x_empty + 8 * kMaxSlots, a_empty = a_full + 8 * kMaxSlots;
-    const uint32_t acc_full = a_empty + 8 * kMaxSlots, acc_empty = acc_full + 8, drain = acc_empty + 8;
+    const uint32_t full = s32(bars), empty = full + 8 * kMaxSlots;  // of both rings' slots
+    const uint32_t acc_full = empty + 8 * kMaxSlots, acc_empty = acc_full + 8, drain = acc_empty + 8;
     const Abort ab{&abort_flag, err};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tile = blockIdx.x / splits, split = blockIdx.x % splits;
@@ -374,10 +380,8 @@ __global__ void __launch_bounds__(kShrinkThreads)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMaxSlots; ++s) {
-            bar_init(x_full + 8 * s, 1);
-            bar_init(x_empty + 8 * s, 1);
-            bar_init(a_full + 8 * s, 1);
-            bar_init(a_empty + 8 * s, 1);
+            bar_init(full + 8 * s, 2);  // the two producers
+            bar_init(empty + 8 * s, 1);
         }
         bar_init(acc_full, 1);
         bar_init(acc_empty, 4);
@@ -385,8 +389,8 @@ __global__ void __launch_bounds__(kShrinkThreads)
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         for (int i = 0; i < early; ++i) {
-            bar_expect(x_full + 8 * i, kXBytes);
-            load_2d(&maps.x, x_full + 8 * i, x_ring + i * kXBytes, (kb0 + i) * 64, static_cast<int>(m0));
+            bar_expect(full + 8 * i, kXBytes);
+            load_2d(&maps.x, full + 8 * i, x_ring + i * kXBytes, (kb0 + i) * 64, static_cast<int>(m0));
         }
     }
     if (warp == 1) {
@@ -415,14 +419,19 @@ __global__ void __launch_bounds__(kShrinkThreads)
             int slot = early % slots, issued = early;
             uint32_t phase = early == slots ? 1 : 0;
             bool ok = passes > 0;
+            // A ring shortened by wide adapters keeps too little of x in flight:
+            // L2 then fetches what the full ring would hold.
+            const int ahead = splits > 1 ? kMaxSlots : 0;
             for (int i = early; i < steps && ok; ++i) {
-                if (!bar_wait(x_empty + 8 * slot, phase ^ 1, ab, 40)) {
+                if (!bar_wait(empty + 8 * slot, phase ^ 1, ab, 40)) {
                     ok = false;
                     break;
                 }
-                bar_expect(x_full + 8 * slot, kXBytes);
-                load_2d(&maps.x, x_full + 8 * slot, x_ring + slot * kXBytes, (kb0 + i % kbs) * 64,
+                bar_expect(full + 8 * slot, kXBytes);
+                load_2d(&maps.x, full + 8 * slot, x_ring + slot * kXBytes, (kb0 + i % kbs) * 64,
                         static_cast<int>(m0));
+                if (ahead > slots && i + ahead - slots < kbs)
+                    prefetch_2d(&maps.x, (kb0 + i + ahead - slots) * 64, static_cast<int>(m0));
                 if (issued < slots) ++issued;
                 if (++slot == slots) {
                     slot = 0;
@@ -431,12 +440,14 @@ __global__ void __launch_bounds__(kShrinkThreads)
             }
             if (!ok) {  // given up, or nothing to multiply: the copies in flight land first
                 const uint64_t deadline = timer_ns() + kTimeoutNs;
+                if (passes == 0)
+                    for (int i = 0; i < early; ++i) bar_arrive(full + 8 * i);  // the other producer's part
                 for (int i = 0; i < issued; ++i) {
                     if (--slot < 0) {
                         slot = slots - 1;
                         phase ^= 1;
                     }
-                    bar_drain(x_full + 8 * slot, phase, deadline);
+                    bar_drain(full + 8 * slot, phase, deadline);
                 }
             }
         }
@@ -448,13 +459,13 @@ __global__ void __launch_bounds__(kShrinkThreads)
             for (int q = 0; q < passes && ok; ++q) {
                 const int d0 = q * group, d1 = min(count, d0 + group);
                 for (int kb = kb0; kb < kb0 + kbs; ++kb) {
-                    if (!bar_wait(a_empty + 8 * slot, phase ^ 1, ab, 40)) {
+                    if (!bar_wait(empty + 8 * slot, phase ^ 1, ab, 40)) {
                         ok = false;
                         break;
                     }
-                    bar_expect(a_full + 8 * slot, (d1 - d0) * rank * 128);
+                    bar_expect(full + 8 * slot, (d1 - d0) * rank * 128);
                     for (int d = d0; d < d1; ++d)
-                        load_2d(&maps.a, a_full + 8 * slot, a_ring + slot * a_slot + (d - d0) * rank * 128,
+                        load_2d(&maps.a, full + 8 * slot, a_ring + slot * a_slot + (d - d0) * rank * 128,
                                 kb * 64, ts.list[d] * rank);
                     if (issued < slots) ++issued;
                     if (++slot == slots) {
@@ -470,7 +481,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
                         slot = slots - 1;
                         phase ^= 1;
                     }
-                    bar_drain(a_full + 8 * slot, phase, deadline);
+                    bar_drain(full + 8 * slot, phase, deadline);
                 }
             }
         }
@@ -485,8 +496,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
                 if (!bar_wait(acc_empty, (q & 1) ^ 1, ab, 41)) break;
                 fence_after();
                 for (int kb = 0; kb < kbs; ++kb) {
-                    if (!bar_wait(a_full + 8 * slot, phase, ab, 42) ||
-                        !bar_wait(x_full + 8 * slot, phase, ab, 42)) {
+                    if (!bar_wait(full + 8 * slot, phase, ab, 42)) {
                         ok = false;
                         break;
                     }
@@ -496,8 +506,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         mma_bf16(tmem, a + 2 * j, b + 2 * j, idesc, (kb > 0 || j > 0) ? 1u : 0u);
-                    mma_commit(x_empty + 8 * slot);
-                    mma_commit(a_empty + 8 * slot);
+                    mma_commit(empty + 8 * slot);
                     if (++slot == slots) {
                         slot = 0;
                         phase ^= 1;
@@ -566,7 +575,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
                          : "memory");
         const TLayout tl(rank);
         const int share = (kTileRows + splits - 1) / splits;
-        for (int i = threadIdx.x; i < share * (rank >> 3); i += kShrinkThreads) {
+        for (int i = threadIdx.x; i < share * (rank >> 3); i += kThreads) {
             const int row = split * share + i % share, r = i / share * 8;
             const int d = row < kTileRows ? ts.row[row] : -1;
             if (d < 0) continue;
@@ -637,6 +646,8 @@ constexpr int kUnitsPerCta = 32;
 
 int expand_unit(int64_t rank) { return rank <= 64 ? 64 : 128; }
 
+constexpr int expand_threads(int unit) { return 32 * (3 + unit / 16); }
+
 ExpandPlan expand_plan(int64_t rank) {
     const TLayout tl(static_cast<int>(rank));
     const int unit = expand_unit(rank);
@@ -654,11 +665,13 @@ ExpandPlan expand_plan(int64_t rank) {
 // The launch's units, row tile by row tile, are dealt out evenly: CTA i of G
 // takes those from units * i / G on, which are parts of one or a few tiles.
 template <int kUnit>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(expand_threads(kUnit))
     lora_expand_kernel(const __grid_constant__ ExpandMaps maps, const nvfp4_lora_args p,
                        const ExpandPlan plan, int *err) {
     constexpr uint32_t kYBytes = kUnit / 64 * kBoxBytes;
     constexpr int kAccs = kAccCols / kUnit;
+    constexpr int kEpiWarps = kUnit / 16;  // four per 64 columns
+    constexpr int kBWarp = 2 + kEpiWarps;  // loads B
     extern __shared__ uint8_t smem_raw[];
     __shared__ TileSlots ts;
     __shared__ __align__(8) uint64_t bars[2 * kMaxYSlots + 2 * kMaxBSlots + 2 * kAccs + 2];
@@ -680,7 +693,7 @@ __global__ void __launch_bounds__(kThreads)
     if (threadIdx.x == 0) {
         for (int s = 0; s < plan.y_slots; ++s) {
             bar_init(y_full + 8 * s, 1);
-            bar_init(y_empty + 8 * s, 4);
+            bar_init(y_empty + 8 * s, kEpiWarps);
         }
         for (int s = 0; s < plan.b_slots; ++s) {
             bar_init(b_full + 8 * s, 1);
@@ -688,7 +701,7 @@ __global__ void __launch_bounds__(kThreads)
         }
         for (int s = 0; s < kAccs; ++s) {
             bar_init(d_full + 8 * s, 1);
-            bar_init(d_empty + 8 * s, 4);
+            bar_init(d_empty + 8 * s, kEpiWarps);
         }
         bar_init(t_full, 1);
         bar_init(drain, 1);
@@ -724,9 +737,8 @@ __global__ void __launch_bounds__(kThreads)
         if (count == 0 && p.out == p.y) continue;  // nothing to add and nothing to copy
 
         if (warp == 0) {
-            if (lane == 0) {
-                bool ok = true;
-                for (int u = u0; u < u1 && ok; ++u) {
+            if (lane == 0)
+                for (int u = u0; u < u1; ++u) {
                     if (!bar_wait(y_empty + 8 * ys, yph ^ 1, ab, 44)) break;
                     bar_expect(y_full + 8 * ys, kYBytes);
 #pragma unroll
@@ -738,6 +750,11 @@ __global__ void __launch_bounds__(kThreads)
                         ys = 0;
                         yph ^= 1;
                     }
+                }
+        } else if (warp == kBWarp) {
+            if (lane == 0) {
+                bool ok = true;
+                for (int u = u0; u < u1 && ok; ++u)
                     for (int d = 0; d < count; ++d) {
                         if (!bar_wait(b_empty + 8 * bs, bph ^ 1, ab, 45)) {
                             ok = false;
@@ -754,7 +771,6 @@ __global__ void __launch_bounds__(kThreads)
                             bph ^= 1;
                         }
                     }
-                }
             }
         } else if (warp == 1) {
             if (lane == 0 && count > 0) {
@@ -800,14 +816,14 @@ __global__ void __launch_bounds__(kThreads)
             }
             __syncwarp();
         } else {
-            const int quad = warp & 3, row = quad * 32 + lane;
+            const int quad = warp & 3, row = quad * 32 + lane, h = (warp - 2) / 4 * 64;
             const int mine = ts.row[row];
             const uint32_t swz = (row & 7) << 4;
             const bool stored = m0 + quad * 32 < p.rows;  // a box of this warp's rows
             bool ok = true;
             for (int u = u0; u < u1; ++u) {
                 if (!bar_wait_warp(y_full + 8 * ys, yph, ab, 47)) break;
-                const uint32_t y = y_ring + ys * kYBytes + row * 128;
+                const uint32_t box = y_ring + ys * kYBytes + h * (kTileRows * 2);
                 for (int d = 0; d < count; ++d) {
                     if (!bar_wait_warp(d_full + 8 * acc, aph, ab, 47)) {
                         ok = false;
@@ -816,30 +832,24 @@ __global__ void __launch_bounds__(kThreads)
                     fence_after();
                     const uint32_t src = tmem + acc * kUnit + (static_cast<uint32_t>(quad * 32) << 16);
                     const bool any = count == 1 || __any_sync(0xFFFFFFFFu, mine == d);  // rows of it
+                    uint32_t f[64];
+                    if (any) tmem_ld64(src + h, f);
+                    fence_before();  // read: back to the MMA thread
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(d_empty + 8 * acc);
+                    if (mine == d) {
 #pragma unroll
-                    for (int h = 0; h < kUnit; h += 64) {
-                        uint32_t f[64];
-                        if (any) tmem_ld64(src + h, f);
-                        if (h + 64 == kUnit) {  // read: back to the MMA thread
-                            fence_before();
-                            __syncwarp();
-                            if (lane == 0) bar_arrive(d_empty + 8 * acc);
+                        for (int c = 0; c < 8; ++c) {
+                            const uint32_t at = box + row * 128 + ((16 * c) ^ swz);
+                            uint4 v = ld_shared_16B(at);
+                            v.x = add_pair(v.x, f[8 * c], f[8 * c + 1]);
+                            v.y = add_pair(v.y, f[8 * c + 2], f[8 * c + 3]);
+                            v.z = add_pair(v.z, f[8 * c + 4], f[8 * c + 5]);
+                            v.w = add_pair(v.w, f[8 * c + 6], f[8 * c + 7]);
+                            st_shared_16B(at, v);
                         }
-                        if (mine == d) {
-                            const uint32_t yh = y + h * (kTileRows * 2);
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                const uint32_t at = yh + ((16 * c) ^ swz);
-                                uint4 v = ld_shared_16B(at);
-                                v.x = add_pair(v.x, f[8 * c], f[8 * c + 1]);
-                                v.y = add_pair(v.y, f[8 * c + 2], f[8 * c + 3]);
-                                v.z = add_pair(v.z, f[8 * c + 4], f[8 * c + 5]);
-                                v.w = add_pair(v.w, f[8 * c + 6], f[8 * c + 7]);
-                                st_shared_16B(at, v);
-                            }
-                        }
-                        __syncwarp();
                     }
+                    __syncwarp();
                     if (++acc == kAccs) {
                         acc = 0;
                         aph ^= 1;
@@ -851,11 +861,8 @@ __global__ void __launch_bounds__(kThreads)
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) {
-#pragma unroll
-                    for (int h = 0; h < kUnit; h += 64)
-                        if (stored && u * kUnit + h < p.n)
-                            store_2d(&maps.out, y_ring + ys * kYBytes + h * (kTileRows * 2) + quad * 4096,
-                                     u * kUnit + h, static_cast<int>(m0) + quad * 32);
+                    if (stored && u * kUnit + h < p.n)
+                        store_2d(&maps.out, box + quad * 4096, u * kUnit + h, static_cast<int>(m0) + quad * 32);
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                     asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
                     if (prev >= 0) bar_arrive(y_empty + 8 * prev);
@@ -873,7 +880,7 @@ __global__ void __launch_bounds__(kThreads)
         if (abort_flag) break;
     }
 
-    if (warp == 0 && lane == 0 && abort_flag) {  // copies still in flight
+    if (lane == 0 && abort_flag) {  // copies still in flight
         const uint64_t deadline = timer_ns() + kTimeoutNs;
         for (int i = 0; i < y_issued; ++i) {
             if (--ys < 0) {
@@ -890,7 +897,7 @@ __global__ void __launch_bounds__(kThreads)
             bar_drain(b_full + 8 * bs, bph, deadline);
         }
     }
-    if (warp >= 2 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (warp >= 2 && warp < kBWarp && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");  // this grid never ends before the shrink
     if (warp == 1) {
         if (lane == 0) {  // every MMA, and t's copies, have completed
@@ -941,7 +948,7 @@ cudaLaunchConfig_t shrink_config(int64_t tiles, int splits, uint32_t rings, cuda
     attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits));
-    cfg.blockDim = dim3(kShrinkThreads);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = rings + 1024;
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -994,7 +1001,7 @@ cudaError_t launch_expand(const ExpandMaps &maps, const nvfp4_lora_args &p, cons
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(expand_threads(kUnit));
     cfg.dynamicSmemBytes = plan.smem_bytes;
     cfg.stream = stream;
     cfg.attrs = &attr;
