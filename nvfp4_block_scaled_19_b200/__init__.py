@@ -14,9 +14,9 @@ missing or the device is not sm_100, calls raise.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import NamedTuple
 
@@ -71,6 +71,18 @@ class LoraArgs(ctypes.Structure):
                 [(n, ctypes.c_void_p) for n in ("a", "b", "scale", "row_slot", "workspace")])
 
 
+def _packer(args) -> struct.Struct:
+    """Packs the fields of an argument structure in order, as C lays it out
+    (several times quicker than setting them one by one)."""
+    codes = {ctypes.c_int64: "q", ctypes.c_void_p: "P", ctypes.c_float: "f", ctypes.c_int: "i"}
+    packer = struct.Struct("@" + "".join(codes[t] for _, t in args._fields_))
+    assert packer.size == ctypes.sizeof(args)
+    return packer
+
+
+_pack_residual_norm = _packer(ResidualNormArgs).pack
+_pack_lora = _packer(LoraArgs).pack
+
 _lib = None
 
 
@@ -115,11 +127,11 @@ def lib() -> ctypes.CDLL:
         L.nvfp4_fp8_gemm.restype = st
         L.nvfp4_fp8_gemm.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, vp, vp]
         L.nvfp4_residual_norm.restype = st
-        L.nvfp4_residual_norm.argtypes = [ctypes.POINTER(ResidualNormArgs), vp]
+        L.nvfp4_residual_norm.argtypes = [vp, vp]  # an nvfp4_residual_norm_args
         L.nvfp4_lora_workspace_bytes.restype = ctypes.c_size_t
         L.nvfp4_lora_workspace_bytes.argtypes = [i64, i64, i64, i64]
         L.nvfp4_lora.restype = st
-        L.nvfp4_lora.argtypes = [ctypes.POINTER(LoraArgs), vp]
+        L.nvfp4_lora.argtypes = [vp, vp]  # an nvfp4_lora_args
         L.nvfp4_selftest_wait_timeout.restype = st
         L.nvfp4_selftest_wait_timeout.argtypes = [i64, vp]
         L.nvfp4_linear_host.restype = st
@@ -450,43 +462,44 @@ class NVFP4Linear:
                 "y": torch.empty(M, self.N, dtype=torch.bfloat16, device=dev)}
 
 
-def _raw_stream(device, stream) -> int:
-    """The given stream, or the current stream of the tensors' device."""
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+def _launch(name: str, args: bytes, index: int, stream) -> None:
+    """Calls an entry point that takes a packed argument structure, on the
+    tensors' device and its current stream (or the given one)."""
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    fn = getattr(lib(), name)
+    if index == torch.cuda.current_device():
+        status = fn(args, raw)
+    else:
+        with torch.cuda.device(index):
+            status = fn(args, raw)
+    if status != 0:
+        raise NVFP4Error(name, status)
 
 
-@contextlib.contextmanager
-def _other_device(device):
-    with torch.cuda.device(device):
-        yield
-
-
-def _on(device):
-    """Makes the tensors' device the current one for a call (the library
-    launches there); nothing to do where it is."""
-    return _NOTHING if device.index == torch.cuda.current_device() else _other_device(device)
-
-
-_NOTHING = contextlib.nullcontext()
-
-
-def _row_stride(t: torch.Tensor, name: str, dtype, rows: int, cols: int, device) -> int:
+def _row_stride(t: torch.Tensor, name: str, dtype, shape, index: int) -> int:
     """Elements from row to row of a [rows, cols] CUDA tensor whose rows are
     contiguous (a column slice of a wider tensor may be passed)."""
-    if t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-        raise ValueError(f"{name} must be a {dtype} [{rows}, {cols}] tensor")
-    if t.device != device or not t.is_cuda:
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name} must be a {dtype} {list(shape)} tensor")
+    if t.get_device() != index:
         raise ValueError(f"{name} must be a CUDA tensor on the device of the others")
     stride, inner = t.stride()
     if inner != 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    return stride if rows > 1 else cols
+    return stride if shape[0] > 1 else shape[1]
 
 
-def _row_index(t: torch.Tensor, name: str, rows: int, device) -> int:
-    if t.dtype != torch.int32 or t.device != device or t.numel() != rows or not t.is_contiguous():
+def _row_index(t: torch.Tensor, name: str, rows: int, index: int) -> int:
+    if t.dtype is not torch.int32 or t.get_device() != index or t.numel() != rows or not t.is_contiguous():
         raise ValueError(f"{name} must hold one int32 per row, on the device of the others")
     return t.data_ptr()
+
+
+def _cuda_index(t: torch.Tensor, name: str) -> int:
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return index
 
 
 @dataclass(slots=True)
@@ -500,6 +513,30 @@ class Norm:
 
 _NORM_KINDS = {"rms": 1, "layer": 2}      # nvfp4_norm values
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1}  # nvfp4_dtype values
+
+
+def _norm_kind(norm: Norm) -> int:
+    kind = _NORM_KINDS.get(norm.kind)
+    if kind is None:
+        raise ValueError("a norm is 'rms' or 'layer'")
+    return kind
+
+
+def _vector(t: torch.Tensor, name: str, dtype, cols: int, index: int, groups: int) -> tuple[int, int, int]:
+    """(pointer, elements from request to request, requests) of a weight or
+    modulation vector; groups: the requests known so far, 0 where the vector
+    cannot have any of its own."""
+    if t.dtype is not dtype or dtype not in _DTYPES:
+        raise ValueError("weights, biases, gate, scale and shift must all be bf16 or all fp32")
+    size, strides = t.shape, t.stride()
+    if t.get_device() != index or not size or size[-1] != cols or strides[-1] != 1:
+        raise ValueError(f"{name} must hold {cols} contiguous values, on the device of the others")
+    if len(size) == 1 or (groups and len(size) == 2 and size[0] == 1):
+        return t.data_ptr(), 0, groups
+    if not groups or len(size) != 2 or groups not in (1, size[0]) or not size[0]:
+        raise ValueError(f"{name} must be [cols]" +
+                         (" or [groups, cols], with the same groups for all" if groups else ""))
+    return t.data_ptr(), strides[0], size[0]
 
 
 class ResidualNorm(NamedTuple):
@@ -536,96 +573,86 @@ def residual_norm(residual: torch.Tensor, y: torch.Tensor | None = None, *,
     Without pre, only h is computed."""
     if residual.dim() != 2 or residual.dtype not in _DTYPES:
         raise ValueError("residual must be a bf16 or fp32 [rows, cols] tensor")
-    rows, cols = residual.shape
-    dev, bf16 = residual.device, torch.bfloat16
-    a = ResidualNormArgs()
-    a.rows, a.cols = rows, cols
-    a.residual_stride = _row_stride(residual, "residual", residual.dtype, rows, cols, dev)
-    a.residual = residual.data_ptr()
-    a.stream_dtype = _DTYPES[residual.dtype]
-    a.residual_scale, a.branch_scale = residual_scale, branch_scale
+    stream_type, shape, bf16 = residual.dtype, residual.shape, torch.bfloat16
+    rows, cols = shape
+    dev = _cuda_index(residual, "residual")
+    r_stride = _row_stride(residual, "residual", stream_type, shape, dev)
+    y_ptr = y_stride = h_ptr = h_stride = out_ptr = out_stride = 0
+    q_ptr = sf_ptr = s_dec_ptr = amax_ptr = 0
     if y is not None:
-        a.y_stride = _row_stride(y, "y", bf16, rows, cols, dev)
-        a.y = y.data_ptr()
+        y_stride = _row_stride(y, "y", bf16, shape, dev)
+        y_ptr = y.data_ptr()
         if h is None and want_h:
-            h = torch.empty(rows, cols, dtype=residual.dtype, device=dev)
+            h = torch.empty(rows, cols, dtype=stream_type, device=residual.device)
     elif post is not None or gate is not None or h is not None:
         raise ValueError("post, gate and h need y")
     if h is not None:
-        a.h_stride = _row_stride(h, "h", residual.dtype, rows, cols, dev)
-        a.h = h.data_ptr()
+        h_stride = _row_stride(h, "h", stream_type, shape, dev)
+        h_ptr = h.data_ptr()
     if pre is None:
         if scale is not None or shift is not None or out is not None or quant is not None or want_quant:
             raise ValueError("scale, shift, out and quant need pre")
     else:
         if out is None and want_out:
-            out = torch.empty(rows, cols, dtype=bf16, device=dev)
+            out = torch.empty(rows, cols, dtype=bf16, device=residual.device)
         if out is not None:
-            a.out_stride = _row_stride(out, "out", bf16, rows, cols, dev)
-            a.out = out.data_ptr()
+            out_stride = _row_stride(out, "out", bf16, shape, dev)
+            out_ptr = out.data_ptr()
         if quant is None and want_quant:
-            quant = empty_nvfp4(rows, cols, dev, row_scales=True)
-        if quant is not None:
+            quant = empty_nvfp4(rows, cols, residual.device, row_scales=True)
+        elif quant is not None:
             if ((quant.rows, quant.cols) != (rows, cols) or quant.s_dec.numel() != rows or
-                    quant.q.device != dev or quant.q.numel() != rows * cols // 2):
+                    quant.q.get_device() != dev or quant.q.numel() != rows * cols // 2 or
+                    quant.sf.numel() != sf_bytes(rows, cols)):
                 raise ValueError("quant must be an NVFP4Tensor of these rows and columns with row scales")
-            a.q, a.sf, a.s_dec_rows = quant.q.data_ptr(), quant.sf.data_ptr(), quant.s_dec.data_ptr()
+        if quant is not None:
+            q_ptr, sf_ptr, s_dec_ptr = quant.q.data_ptr(), quant.sf.data_ptr(), quant.s_dec.data_ptr()
     if amax_rows is not None:
         if (quant is None or amax_rows.numel() != rows or amax_rows.dtype != torch.float32 or
-                amax_rows.device != dev or not amax_rows.is_contiguous()):
+                amax_rows.get_device() != dev or not amax_rows.is_contiguous()):
             raise ValueError("amax_rows must hold one fp32 per row, and needs quant")
-        a.amax_rows = amax_rows.data_ptr()
+        amax_ptr = amax_rows.data_ptr()
 
-    vec_dtype, groups = None, 1
-
-    def vector(t, name):
-        nonlocal vec_dtype, groups
-        if t.dtype not in _DTYPES or (vec_dtype is not None and t.dtype != vec_dtype):
-            raise ValueError("weights, biases, gate, scale and shift must all be bf16 or all fp32")
-        vec_dtype = t.dtype
-        if t.device != dev or t.shape[-1] != cols or t.stride(-1) != 1:
-            raise ValueError(f"{name} must hold {cols} contiguous values, on the device of the others")
-        if t.dim() == 1:
-            return 0
-        if t.dim() != 2 or name.endswith(("weight", "bias")) or (groups not in (1, t.shape[0])):
-            raise ValueError(f"{name} must be [cols]" +
-                             ("" if name.endswith(("weight", "bias")) else " or [groups, cols], one groups for all"))
-        if t.shape[0] == 1:
-            return 0
-        groups = t.shape[0]
-        return t.stride(0)
-
-    for name, norm in (("post", post), ("pre", pre)):
-        if norm is None:
-            continue
-        if norm.kind not in _NORM_KINDS:
-            raise ValueError(f"{name}: a norm is 'rms' or 'layer'")
-        setattr(a, name + "_norm", _NORM_KINDS[norm.kind])
-        setattr(a, name + "_eps", norm.eps)
-        if norm.weight is not None:
-            vector(norm.weight, name + ".weight")
-            setattr(a, name + "_weight", norm.weight.data_ptr())
-        if norm.bias is not None:
-            vector(norm.bias, name + ".bias")
-            setattr(a, name + "_bias", norm.bias.data_ptr())
+    vec_type, groups = None, 1
+    post_kind = pre_kind = post_w = post_b = pre_w = pre_b = 0
+    post_eps = pre_eps = 0.0
+    gate_ptr = gate_stride = scale_ptr = scale_stride = shift_ptr = shift_stride = 0
+    if post is not None:
+        post_kind, post_eps = _norm_kind(post), post.eps
+        if post.weight is not None:
+            vec_type = post.weight.dtype
+            post_w = _vector(post.weight, "post.weight", vec_type, cols, dev, 0)[0]
+        if post.bias is not None:
+            vec_type = vec_type or post.bias.dtype
+            post_b = _vector(post.bias, "post.bias", vec_type, cols, dev, 0)[0]
+    if pre is not None:
+        pre_kind, pre_eps = _norm_kind(pre), pre.eps
+        if pre.weight is not None:
+            vec_type = vec_type or pre.weight.dtype
+            pre_w = _vector(pre.weight, "pre.weight", vec_type, cols, dev, 0)[0]
+        if pre.bias is not None:
+            vec_type = vec_type or pre.bias.dtype
+            pre_b = _vector(pre.bias, "pre.bias", vec_type, cols, dev, 0)[0]
     if gate is not None:
-        a.gate_stride = vector(gate, "gate")
-        a.gate = gate.data_ptr()
+        vec_type = vec_type or gate.dtype
+        gate_ptr, gate_stride, groups = _vector(gate, "gate", vec_type, cols, dev, groups)
     if scale is not None:
-        a.scale_stride = vector(scale, "scale")
-        a.scale = scale.data_ptr()
+        vec_type = vec_type or scale.dtype
+        scale_ptr, scale_stride, groups = _vector(scale, "scale", vec_type, cols, dev, groups)
     if shift is not None:
-        a.shift_stride = vector(shift, "shift")
-        a.shift = shift.data_ptr()
-    a.vector_dtype = _DTYPES[vec_dtype] if vec_dtype is not None else 0
-    a.groups = groups
+        vec_type = vec_type or shift.dtype
+        shift_ptr, shift_stride, groups = _vector(shift, "shift", vec_type, cols, dev, groups)
+    index = 0
     if row_group is not None:
-        a.row_group = _row_index(row_group, "row_group", rows, dev)
+        index = _row_index(row_group, "row_group", rows, dev)
         if groups == 1:  # no vector of a request's own: every number from 0 on is one
-            a.groups = 1 << 31
-    with _on(dev):
-        _check("nvfp4_residual_norm",
-               lib().nvfp4_residual_norm(ctypes.byref(a), _raw_stream(dev, stream)))
+            groups = 1 << 31
+    args = _pack_residual_norm(
+        rows, cols, residual.data_ptr(), r_stride, y_ptr, y_stride, h_ptr, h_stride, out_ptr, out_stride,
+        post_w, post_b, pre_w, pre_b, gate_ptr, gate_stride, scale_ptr, scale_stride, shift_ptr, shift_stride,
+        index, groups, q_ptr, sf_ptr, s_dec_ptr, amax_ptr, residual_scale, branch_scale, post_eps, pre_eps,
+        post_kind, pre_kind, _DTYPES[stream_type], 0 if vec_type is None else _DTYPES[vec_type])
+    _launch("nvfp4_residual_norm", args, dev, stream)
     return ResidualNorm(h, out, quant)
 
 
@@ -672,40 +699,35 @@ def lora(x: torch.Tensor, y: torch.Tensor, adapters: LoraAdapters,
     order; a number outside [0, slots) means no adapter (out = y).  None: slot 0
     for every row.  out may be y itself; a new tensor if not given."""
     a, b, scale = adapters.a, adapters.b, adapters.scale
-    if a.dim() != 3 or b.dim() != 3:
-        raise ValueError("adapters.a is [slots, rank, K], adapters.b [slots, N, rank]")
+    bf16, dev = torch.bfloat16, _cuda_index(x, "x")
+    if a.dim() != 3 or b.dim() != 3 or x.dim() != 2:
+        raise ValueError("x is [rows, K], adapters.a [slots, rank, K], adapters.b [slots, N, rank]")
     slots, rank, k = a.shape
-    n, dev, bf16 = b.shape[1], x.device, torch.bfloat16
-    if (a.dtype != bf16 or b.dtype != bf16 or scale.dtype != torch.float32 or
+    rows, n = x.shape[0], b.shape[1]
+    if (a.dtype is not bf16 or b.dtype is not bf16 or scale.dtype is not torch.float32 or
+            b.shape != (slots, n, rank) or scale.shape != (slots,) or
             not (a.is_contiguous() and b.is_contiguous() and scale.is_contiguous()) or
-            b.shape[0] != slots or b.shape[2] != rank or scale.numel() != slots or
-            a.device != dev or b.device != dev or scale.device != dev):
+            a.get_device() != dev or b.get_device() != dev or scale.get_device() != dev):
         raise ValueError("adapters must be contiguous bf16 a [slots, rank, K] and b [slots, N, rank] "
                          "and fp32 scale [slots], on the device of x")
-    rows = x.shape[0]
-    p = LoraArgs()
-    p.rows, p.k, p.n, p.rank, p.slots = rows, k, n, rank, slots
-    p.x_stride = _row_stride(x, "x", bf16, rows, k, dev)
-    p.y_stride = _row_stride(y, "y", bf16, rows, n, dev)
+    x_stride = _row_stride(x, "x", bf16, (rows, k), dev)
+    y_stride = _row_stride(y, "y", bf16, (rows, n), dev)
     if out is None:
-        out = torch.empty(rows, n, dtype=bf16, device=dev)
-    p.out_stride = _row_stride(out, "out", bf16, rows, n, dev)
-    p.x, p.y, p.out = x.data_ptr(), y.data_ptr(), out.data_ptr()
-    p.a, p.b, p.scale = a.data_ptr(), b.data_ptr(), scale.data_ptr()
-    if row_slot is not None:
-        p.row_slot = _row_index(row_slot, "row_slot", rows, dev)
-    with _on(dev):
-        need = lib().nvfp4_lora_workspace_bytes(rows, k, n, rank)
-        if need:
-            if workspace is None:
-                # Of the stream it is used on, so that it is free again in that stream's order.
-                with torch.cuda.stream(stream):
-                    workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-            elif workspace.device != dev or not workspace.is_contiguous() or \
-                    workspace.numel() * workspace.element_size() < need:
-                raise ValueError(f"workspace must hold {need} contiguous bytes on the device of x")
-            p.workspace = workspace.data_ptr()
-        _check("nvfp4_lora", lib().nvfp4_lora(ctypes.byref(p), _raw_stream(dev, stream)))
+        out = torch.empty(rows, n, dtype=bf16, device=x.device)
+    out_stride = y_stride if out is y else _row_stride(out, "out", bf16, (rows, n), dev)
+    index = 0 if row_slot is None else _row_index(row_slot, "row_slot", rows, dev)
+    need = lib().nvfp4_lora_workspace_bytes(rows, k, n, rank)
+    if need and workspace is None:
+        # Of the stream it is used on, so that it is free again in that stream's order.
+        with torch.cuda.stream(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    elif need and (workspace.get_device() != dev or not workspace.is_contiguous() or
+                   workspace.numel() * workspace.element_size() < need):
+        raise ValueError(f"workspace must hold {need} contiguous bytes on the device of x")
+    args = _pack_lora(rows, k, n, rank, slots, x.data_ptr(), x_stride, y.data_ptr(), y_stride,
+                      out.data_ptr(), out_stride, a.data_ptr(), b.data_ptr(), scale.data_ptr(), index,
+                      workspace.data_ptr() if need else 0)
+    _launch("nvfp4_lora", args, dev, stream)
     return out
 
 
