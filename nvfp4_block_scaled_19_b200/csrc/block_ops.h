@@ -20,8 +20,12 @@ size_t lora_workspace_bytes(int64_t rows, int64_t k, int64_t n, int64_t rank);
 // A checked adapter call (see nvfp4_lora_args); rows > 0.
 cudaError_t launch_lora(const nvfp4_lora_args &p, cudaStream_t stream);
 
-// The same for many rows, on 128-row tensor-core tiles (lora_tile.cu).
+// The same for many rows, on 128-row tensor-core tiles (lora_tile.cu).  A tile
+// whose rows have more than most_adapters different ones is left out, with a 1
+// in its place of the array that *crowded receives (one int per tile, in the
+// workspace).
 size_t lora_tile_workspace_bytes(int64_t rows, int64_t rank);
-cudaError_t launch_lora_tile(const nvfp4_lora_args &p, cudaStream_t stream);
+cudaError_t launch_lora_tile(const nvfp4_lora_args &p, int most_adapters, const int **crowded,
+                             cudaStream_t stream);
 
 }  // namespace nvfp4

@@ -78,7 +78,7 @@ __device__ __forceinline__ float dot8(const float *t, uint4 b, float acc) {
 // of a warp, and U batches are in flight at a time.
 template <int R16>
 __global__ void __launch_bounds__(kRowThreads, R16 <= 2 ? 4 : R16 == 4 ? 3 : 2) __cluster_dims__(kCluster, 1, 1)
-    lora_rows_kernel(const nvfp4_lora_args p) {
+    lora_rows_kernel(const nvfp4_lora_args p, const int *crowded) {
     constexpr int rank = 16 * R16;
     constexpr int L = R16 == 8 ? 16 : R16 == 4 ? 8 : R16 % 2 == 0 ? 4 : 2;
     constexpr int V = rank / 8 / L;
@@ -88,6 +88,8 @@ __global__ void __launch_bounds__(kRowThreads, R16 <= 2 ? 4 : R16 == 4 ? 3 : 2) 
     const int64_t row = blockIdx.x / kCluster;
     const int c = static_cast<int>(blockIdx.x % kCluster);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // Beside the tile kernels: only the rows of the tiles they left out.
+    if (crowded != nullptr && __ldg(crowded + (row >> 7)) == 0) return;
     const uint16_t *yrow = static_cast<const uint16_t *>(p.y) + row * p.y_stride;
     uint16_t *orow = static_cast<uint16_t *>(p.out) + row * p.out_stride;
     // This CTA's outputs.
@@ -200,34 +202,54 @@ __global__ void __launch_bounds__(kRowThreads, R16 <= 2 ? 4 : R16 == 4 ? 3 : 2) 
 }
 
 template <int R16>
-cudaError_t launch_rows(const nvfp4_lora_args &p, cudaStream_t stream) {
-    lora_rows_kernel<R16><<<static_cast<unsigned>(p.rows * kCluster), kRowThreads, 0, stream>>>(p);
+cudaError_t launch_rows_as(const nvfp4_lora_args &p, const int *crowded, cudaStream_t stream) {
+    lora_rows_kernel<R16><<<static_cast<unsigned>(p.rows * kCluster), kRowThreads, 0, stream>>>(p, crowded);
     return cudaGetLastError();
+}
+
+cudaError_t launch_rows(const nvfp4_lora_args &p, const int *crowded, cudaStream_t stream) {
+    switch (p.rank / 16) {
+        case 1: return launch_rows_as<1>(p, crowded, stream);
+        case 2: return launch_rows_as<2>(p, crowded, stream);
+        case 3: return launch_rows_as<3>(p, crowded, stream);
+        case 4: return launch_rows_as<4>(p, crowded, stream);
+        case 5: return launch_rows_as<5>(p, crowded, stream);
+        case 6: return launch_rows_as<6>(p, crowded, stream);
+        case 7: return launch_rows_as<7>(p, crowded, stream);
+        default: return launch_rows_as<8>(p, crowded, stream);
+    }
+}
+
+// Whether a cluster per row is taken (us measured with it / on tiles, K = 4096):
+//   rows x rank x (K + N) up to 2^25    rank 16, 64 rows, N 12288: 8.1 / 11.3;
+//     128 rows: 14.3 / 11.5 with one adapter, 14.3 / 15.1 with four;
+//     rank 64, 32 rows, N 12288: 11.2 / 12.9, 64 rows: 24.4 / 13.0
+//   up to 2^26 where many adapters are held: a tile's cost grows with the
+//     adapters among its rows (rank 16, 128 rows with one each: 15.5 / 163),
+//     which the host cannot see
+//   at most 256 rows: each is a cluster, whatever its size.
+bool by_rows(int64_t rows, int64_t k, int64_t n, int64_t rank, bool many_adapters) {
+    return rows <= 256 && rows * rank * (k + n) <= (int64_t(1) << (many_adapters ? 26 : 25));
 }
 
 }  // namespace
 
-// Rows from which the tiles are taken.
-constexpr int64_t kTileFromRows = 97;
-
 size_t lora_workspace_bytes(int64_t rows, int64_t k, int64_t n, int64_t rank) {
-    (void)k;
-    (void)n;
-    return rows < kTileFromRows ? 0 : lora_tile_workspace_bytes(rows, rank);
+    return by_rows(rows, k, n, rank, false) ? 0 : lora_tile_workspace_bytes(rows, rank);
 }
 
 cudaError_t launch_lora(const nvfp4_lora_args &p, cudaStream_t stream) {
-    if (p.rows >= kTileFromRows) return launch_lora_tile(p, stream);
-    switch (p.rank / 16) {
-        case 1: return launch_rows<1>(p, stream);
-        case 2: return launch_rows<2>(p, stream);
-        case 3: return launch_rows<3>(p, stream);
-        case 4: return launch_rows<4>(p, stream);
-        case 5: return launch_rows<5>(p, stream);
-        case 6: return launch_rows<6>(p, stream);
-        case 7: return launch_rows<7>(p, stream);
-        default: return launch_rows<8>(p, stream);
-    }
+    if (by_rows(p.rows, p.k, p.n, p.rank, p.slots > 8)) return launch_rows(p, nullptr, stream);
+    // A tile of D adapters costs about as much as D / 10 tiles row by row (us, 128
+    // rows with an adapter each, by rows / on a tile: rank 16 10 / 158, rank 64
+    // 30 / 276, rank 128 56 / 488), and tiles run side by side: up to 12 of them,
+    // those with more than ten adapters for each tile of the call go row by row.
+    const int64_t tiles = (p.rows + 127) / 128;
+    const int most = static_cast<int>(10 * tiles < 128 ? 10 * tiles : 128);
+    const int *crowded = nullptr;
+    const cudaError_t e = launch_lora_tile(p, most, &crowded, stream);
+    if (e != cudaSuccess || most == 128 || p.slots <= most) return e;
+    return launch_rows(p, crowded, stream);
 }
 
 }  // namespace nvfp4

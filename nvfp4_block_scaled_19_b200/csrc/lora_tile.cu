@@ -355,8 +355,8 @@ constexpr int kMaxSlots = 8;
 
 __global__ void __launch_bounds__(kThreads)
     lora_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const nvfp4_lora_args p,
-                       const int splits, const uint32_t ring_bytes, float *partial, uint16_t *t,
-                       int *err) {
+                       const int splits, const uint32_t ring_bytes, const int most_adapters,
+                       int *crowded, float *partial, uint16_t *t, int *err) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ TileSlots ts;
     __shared__ float scales[kTileRows];
@@ -406,7 +406,9 @@ __global__ void __launch_bounds__(kThreads)
     // The expand may start its prologue once every CTA here holds its tensor memory.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tmem = tmem_holder;
-    const int count = ts.count;
+    // A crowded tile is left to the kernel of single rows.
+    const int count = ts.count <= most_adapters ? ts.count : 0;
+    if (split == 0 && threadIdx.x == 64) crowded[tile] = ts.count > most_adapters;
     const int group = max(1, min(kAccCols / rank, count));  // adapters per pass over x
     const int passes = (count + group - 1) / group;          // 0: no row has an adapter
     const uint32_t a_slot = group * rank * 128;              // at most 32 KB
@@ -577,7 +579,7 @@ __global__ void __launch_bounds__(kThreads)
         const int share = (kTileRows + splits - 1) / splits;
         for (int i = threadIdx.x; i < share * (rank >> 3); i += kThreads) {
             const int row = split * share + i % share, r = i / share * 8;
-            const int d = row < kTileRows ? ts.row[row] : -1;
+            const int d = row < kTileRows && passes > 0 ? ts.row[row] : -1;
             if (d < 0) continue;
             float4 w[kMaxSplits][2];  // asked for together
             if (passes == 1) {
@@ -667,7 +669,7 @@ ExpandPlan expand_plan(int64_t rank) {
 template <int kUnit>
 __global__ void __launch_bounds__(expand_threads(kUnit))
     lora_expand_kernel(const __grid_constant__ ExpandMaps maps, const nvfp4_lora_args p,
-                       const ExpandPlan plan, int *err) {
+                       const ExpandPlan plan, const int most_adapters, int *err) {
     constexpr uint32_t kYBytes = kUnit / 64 * kBoxBytes;
     constexpr int kAccs = kAccCols / kUnit;
     constexpr int kEpiWarps = kUnit / 16;  // four per 64 columns
@@ -735,6 +737,7 @@ __global__ void __launch_bounds__(expand_threads(kUnit))
         find_slots(ts, p, m0);  // begins after every role's end of the last tile, see below
         const int count = ts.count;
         if (count == 0 && p.out == p.y) continue;  // nothing to add and nothing to copy
+        if (count > most_adapters) continue;       // left to the kernel of single rows
 
         if (warp == 0) {
             if (lane == 0)
@@ -990,7 +993,7 @@ int shrink_splits(int64_t rows, int64_t k) {
 
 template <int kUnit>
 cudaError_t launch_expand(const ExpandMaps &maps, const nvfp4_lora_args &p, const ExpandPlan &plan,
-                          int64_t at_once, int *err, cudaStream_t stream) {
+                          int64_t at_once, int most_adapters, int *err, cudaStream_t stream) {
     const cudaError_t e = allow_smem(lora_expand_kernel<kUnit>, plan.smem_bytes);
     if (e != cudaSuccess) return e;
     const int64_t units = row_tiles(p.rows) * ((p.n + kUnit - 1) / kUnit);
@@ -1006,7 +1009,7 @@ cudaError_t launch_expand(const ExpandMaps &maps, const nvfp4_lora_args &p, cons
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, lora_expand_kernel<kUnit>, maps, p, plan, err);
+    return cudaLaunchKernelEx(&cfg, lora_expand_kernel<kUnit>, maps, p, plan, most_adapters, err);
 }
 
 // Room for every split's fp32 sums: splits times the row tiles are at most an SM
@@ -1016,21 +1019,27 @@ size_t partial_bytes(int64_t rows, int64_t rank) {
     return most <= 1 ? 0 : static_cast<size_t>(most * rows * rank) * sizeof(float);
 }
 
+size_t flag_bytes(int64_t rows) { return static_cast<size_t>((row_tiles(rows) + 3) / 4) * 16; }
+
 }  // namespace
 
 size_t lora_tile_workspace_bytes(int64_t rows, int64_t rank) {
     const TLayout tl(static_cast<int>(rank));
-    return partial_bytes(rows, rank) +
-           static_cast<size_t>(rows) * static_cast<size_t>(tl.groups) * 128;
+    return partial_bytes(rows, rank) + static_cast<size_t>(rows) * static_cast<size_t>(tl.groups) * 128 +
+           flag_bytes(rows);
 }
 
-cudaError_t launch_lora_tile(const nvfp4_lora_args &p, cudaStream_t stream) {
+cudaError_t launch_lora_tile(const nvfp4_lora_args &p, int most_adapters, const int **crowded_out,
+                             cudaStream_t stream) {
     int *err = device_error_word();
     if (err == nullptr) return cudaErrorUnknown;
     const TLayout tl(static_cast<int>(p.rank));
     float *partial = static_cast<float *>(p.workspace);
     uint16_t *t = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(p.workspace) +
                                                partial_bytes(p.rows, p.rank));
+    int *crowded = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(t) +
+                                           static_cast<size_t>(p.rows) * tl.groups * 128);
+    *crowded_out = crowded;
     const ExpandPlan plan = expand_plan(p.rank);
     ShrinkMaps sm;
     ExpandMaps em;
@@ -1050,10 +1059,11 @@ cudaError_t launch_lora_tile(const nvfp4_lora_args &p, cudaStream_t stream) {
     const uint32_t rings = tiles * splits <= kSms ? kLargeRings : kSmallRings;
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = shrink_config(tiles, splits, rings, &attr, stream);
-    e = cudaLaunchKernelEx(&cfg, lora_shrink_kernel, sm, p, splits, rings, partial, t, err);
+    e = cudaLaunchKernelEx(&cfg, lora_shrink_kernel, sm, p, splits, rings, most_adapters, crowded, partial, t,
+                           err);
     if (e != cudaSuccess) return e;
-    return expand_unit(p.rank) == 64 ? launch_expand<64>(em, p, plan, 2 * kSms, err, stream)
-                                     : launch_expand<128>(em, p, plan, kSms, err, stream);
+    return expand_unit(p.rank) == 64 ? launch_expand<64>(em, p, plan, 2 * kSms, most_adapters, err, stream)
+                                     : launch_expand<128>(em, p, plan, kSms, most_adapters, err, stream);
 }
 
 }  // namespace nvfp4

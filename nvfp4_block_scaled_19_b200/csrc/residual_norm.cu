@@ -781,8 +781,15 @@ cudaError_t launch_rows(const nvfp4_residual_norm_args &a, int num_sms, cudaStre
 cudaError_t launch_residual_norm(const nvfp4_residual_norm_args &a, int num_sms,
                                  cudaStream_t stream) {
     const int64_t c = a.cols;
-    if (a.rows > 2 * int64_t(num_sms) && c > 256 && c <= 8192) return launch_rows(a, num_sms, stream);
-    // Few rows: one vector per thread, the shortest chain.
+    // The persistent form from 2^21 values on, and from a row per SM where a row
+    // needs more than 512 threads of the other (us, layer norm with gate and
+    // modulation, one CTA per row / persistent: 1200 x 1024 3.7 / 4.1, 2400 x 1024
+    // 6.5 / 5.9; 600 x 2048 3.9 / 4.1, 1200 x 2048 6.6 / 6.0; 444 x 4096 5.0 / 5.1,
+    // 8000 x 4096 64 / 46; 148 x 8192 4.6 / 4.4, 8000 x 8192 185 / 91).  Rows of 256
+    // columns are a warp each.
+    if (c > 256 && c <= 8192 && (c <= 4096 ? a.rows * c > (1 << 21) : a.rows > num_sms))
+        return launch_rows(a, num_sms, stream);
+    // One CTA per row, one vector per thread: the shortest chain.
     if (c <= 256) return launch<32, 1, 4>(a, stream);
     if (c <= 1024) return launch<128, 1, 1>(a, stream);
     if (c <= 2048) return launch<256, 1, 1>(a, stream);

@@ -113,8 +113,13 @@ def test_lora_aliases_and_alignment(nv, p):
 def test_lora_workspace_sizes(nv):
     f = nv.lib().nvfp4_lora_workspace_bytes
     assert f(-1, 64, 64, 16) == 0 and f(4096, 72, 64, 16) == 0 and f(4096, 64, 64, 144) == 0
-    for rows in (0, 1, 100, 5000, 1 << 27):     # room for fp32 partial sums, or none
-        assert f(rows, 4096, 4096, 64) % (4 * 64) == 0
+    assert f(0, 4096, 4096, 64) == f(1, 4096, 4096, 128) == f(64, 4096, 4096, 64) == 0   # row by row
+    for rows in (257, 5000, 1 << 27):
+        # On tiles: the inner vectors as two bf16, a flag per tile, and fp32 sums of
+        # the splits of K, of which there are at most as many as SMs.
+        least = rows * 4 * 64 + (rows + 127) // 128 * 4
+        assert least <= f(rows, 4096, 4096, 64) <= least + 148 * 128 * 64 * 4 + 16
+        assert f(rows, 4096, 4096, 64) % 16 == 0
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-device answer")

@@ -44,16 +44,17 @@ def _check(nv, x, y, ad, slot, **kw):
 ROWS = [1, 2, 7, 33, 64, 65, 128, 129, 200, 257, 513, 1000]
 
 
+@pytest.mark.parametrize("k,n", [(1040, 1544), (5008, 6152)])   # by rows and on tiles
 @pytest.mark.parametrize("rows", ROWS)
 @pytest.mark.parametrize("rank", [16, 32, 48, 64, 80, 96, 112, 128])
-def test_rows_and_ranks(nv, rows, rank):
-    x, y, ad, slot = _inputs(nv, rows, 1040, 1544, rank, 5)
+def test_rows_and_ranks(nv, rows, rank, k, n):
+    x, y, ad, slot = _inputs(nv, rows, k, n, rank, 5)
     _check(nv, x, y, ad, slot)                              # any order
     _check(nv, x, y, ad, slot.sort().values.contiguous())   # requests in a row
     _check(nv, x, y, ad, None)                              # one adapter for all
 
 
-@pytest.mark.parametrize("rows", [1, 100, 300])
+@pytest.mark.parametrize("rows", [1, 100, 260, 300])
 @pytest.mark.parametrize("k,n", [(16, 16), (16, 4096), (4096, 16), (48, 24), (64, 64), (80, 72), (112, 1000),
                                  (4112, 264), (12288, 4096), (2048, 12296)])
 def test_shapes(nv, rows, k, n):
@@ -67,6 +68,23 @@ def test_an_adapter_for_every_row(nv, rows, slots):
     g.manual_seed(1)
     slot = torch.randperm(max(rows, slots), generator=g, device="cuda")[:rows].remainder(slots).to(torch.int32)
     _check(nv, x, y, ad, slot)
+
+
+@pytest.mark.parametrize("rank", [16, 80])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_crowded_tiles_beside_others(nv, rank, in_place):
+    """Tiles of many adapters, of one, of a few and of none in one call."""
+    rows, slots = 640, 100
+    x, y, ad, _ = _inputs(nv, rows, 1024, 2056, rank, slots)
+    slot = torch.full((rows,), -1, dtype=torch.int32, device="cuda")
+    slot[:100] = torch.arange(100, device="cuda", dtype=torch.int32)   # and 28 rows without
+    slot[128:256] = 7
+    slot[384:520] = torch.arange(136, device="cuda", dtype=torch.int32) // 40
+    slot[520:] = torch.arange(120, device="cuda", dtype=torch.int32).flip(0) % slots
+    _check(nv, x, y, ad, slot)
+    if in_place:
+        want, err = lora64(x, y, ad, slot)
+        assert_close(nv.lora(x, y, ad, slot, out=y), want, err)
 
 
 @pytest.mark.parametrize("rows", [3, 300])
