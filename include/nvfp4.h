@@ -354,7 +354,8 @@ nvfp4_status nvfp4_residual_norm(const nvfp4_residual_norm_args *args, nvfp4_str
  *   rank         16 .. 128, rank % 16 == 0 (pad smaller ones with zeros)
  *   slots        adapters held, 1 <= slots, slots * max(k, n, rank) < 2^31
  *   x, y, out    device, bf16 [rows, k], [rows, n], [rows, n]; strides in
- *                elements from row to row, a multiple of 8, at least k or n.
+ *                elements from row to row, a multiple of 8, at least k or n,
+ *                below 2^39.
  *                out may be y itself; otherwise it must not overlap the inputs.
  *   a, b         device, bf16 [slots, rank, k] and [slots, n, rank], contiguous
  *   scale        device, slots fp32

@@ -31,6 +31,13 @@ bool norm_ok(int kind, float eps, const void *weight, const void *bias) {
     return std::isfinite(eps) && eps >= 0.0f;
 }
 
+// The status of a launch; a refused one leaves no error behind for others to find.
+nvfp4_status launched(cudaError_t e) {
+    if (e == cudaSuccess) return NVFP4_OK;
+    cudaGetLastError();
+    return NVFP4_ERR_LAUNCH;
+}
+
 bool lora_sizes_ok(int64_t rows, int64_t k, int64_t n, int64_t rank) {
     return rows >= 0 && rows <= (int64_t(1) << 27) && k >= 16 && k <= (1 << 20) && k % 16 == 0 &&
            n >= 16 && n <= (1 << 20) && n % 8 == 0 && rank >= 16 && rank <= 128 && rank % 16 == 0;
@@ -88,7 +95,7 @@ nvfp4_status nvfp4_residual_norm(const nvfp4_residual_norm_args *args, nvfp4_str
     const nvfp4_status st = nvfp4::current_device(&sms);
     if (st != NVFP4_OK) return st;
     if (a.rows == 0) return NVFP4_OK;
-    return nvfp4::launch_residual_norm(a, sms, stream) == cudaSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
+    return launched(nvfp4::launch_residual_norm(a, sms, stream));
 }
 
 size_t nvfp4_lora_workspace_bytes(int64_t rows, int64_t k, int64_t n, int64_t rank) {
@@ -106,6 +113,10 @@ nvfp4_status nvfp4_lora(const nvfp4_lora_args *args, nvfp4_stream_t stream) {
     if (p.a == nullptr || p.b == nullptr || p.scale == nullptr) return NVFP4_ERR_INVALID_ARG;
     if (p.rows > 0 && (p.x == nullptr || p.y == nullptr || p.out == nullptr || p.out == p.x))
         return NVFP4_ERR_INVALID_ARG;
+    // (A tensor map takes strides below 2^40 bytes.)
+    const int64_t strides[] = {p.x_stride, p.y_stride, p.out_stride};
+    for (const int64_t s : strides)
+        if (s >= int64_t(1) << 39) return NVFP4_ERR_INVALID_ARG;
     if (!stride_ok(p.x_stride, p.rows, p.k) || !stride_ok(p.y_stride, p.rows, p.n) ||
         !stride_ok(p.out_stride, p.rows, p.n))
         return NVFP4_ERR_INVALID_ARG;
@@ -120,7 +131,7 @@ nvfp4_status nvfp4_lora(const nvfp4_lora_args *args, nvfp4_stream_t stream) {
     const nvfp4_status st = nvfp4::current_device(&sms);
     if (st != NVFP4_OK) return st;
     if (p.rows == 0) return NVFP4_OK;
-    return nvfp4::launch_lora(p, stream) == cudaSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
+    return launched(nvfp4::launch_lora(p, stream));
 }
 
 }  // extern "C"

@@ -92,7 +92,7 @@ def _lora_args(nv, p, **kw):
     dict(rows=-1), dict(rows=(1 << 27) + 1), dict(k=0), dict(k=72), dict(k=(1 << 20) + 16), dict(n=8), dict(n=84),
     dict(n=(1 << 20) + 8), dict(rank=0), dict(rank=8), dict(rank=24), dict(rank=144), dict(slots=0),
     dict(slots=1 << 25), dict(x=None), dict(y=None), dict(out=None), dict(a=None), dict(b=None), dict(scale=None),
-    dict(x_stride=56), dict(x_stride=68), dict(y_stride=72), dict(out_stride=0), dict(out_stride=1 << 59),
+    dict(x_stride=56), dict(x_stride=68), dict(y_stride=72), dict(out_stride=0), dict(out_stride=1 << 39),
     dict(rows=1 << 16, workspace=None), dict(k=16, n=16, x_stride=16, rank=128, slots=1 << 25),
 ], ids=str)
 def test_lora_invalid(nv, p, kw):
