@@ -8,8 +8,9 @@
 // warp per rank, so a row of A is read in whole lines), the partial sums go to
 // every CTA of the cluster through distributed shared memory, and after one
 // cluster barrier each CTA adds its slice of N.  B's slice is asked into L2 as
-// soon as A has arrived, behind the reductions and the barrier; asked for with
-// A, it delays A, which everything waits for.
+// soon as A has arrived, behind the reductions and the barrier; asked for before
+// A it delays A, which everything waits for (61 rows, rank 32, K 4096, N 12288:
+// 18.8 us against 16.5; behind A's loads, before they arrive, 17.6).
 // What bounds it: the adapters' bytes, rank * (K + N) * 2 per row, from HBM
 // where rows have adapters of their own and from L2 where they share them.
 #include <cuda_bf16.h>
@@ -47,6 +48,15 @@ __device__ __forceinline__ void cluster_arrive() {
 
 __device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// A load that is issued where it stands.
+__device__ __forceinline__ uint4 ld_nc_16B(const uint4 *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
 }
 
 // acc + a . b over eight bf16 pairs, in order.
@@ -118,17 +128,25 @@ __global__ void __launch_bounds__(kRowThreads, R16 <= 2 ? 4 : R16 == 4 ? 3 : 2) 
         float s[G];
 #pragma unroll
         for (int i = 0; i < G; ++i) s[i] = 0.0f;
-#pragma unroll 2
-        for (int64_t k = k0 + lane; k < k1; k += 32) {
-            const uint4 xv = __ldg(xrow + k);
-            uint4 v[G];
+        for (int64_t k = k0 + lane; k < k1; k += 64) {
+            // Two steps' loads together.
+            uint4 xv[2], v[2][G];
 #pragma unroll
-            for (int i = 0; i < G; ++i)
-                if (i0 + i < kRanks)
-                    v[i] = __ldg(reinterpret_cast<const uint4 *>(a + (warp + (i0 + i) * kRowWarps) * p.k) + k);
+            for (int h = 0; h < 2; ++h) {
+                const bool in = k + 32 * h < k1;
+                xv[h] = in ? ld_nc_16B(xrow + k + 32 * h) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int i = 0; i < G; ++i)
-                if (i0 + i < kRanks) s[i] = dot8(xv, v[i], s[i]);
+                for (int i = 0; i < G; ++i)
+                    v[h][i] = in && i0 + i < kRanks
+                                  ? ld_nc_16B(reinterpret_cast<const uint4 *>(
+                                                  a + (warp + (i0 + i) * kRowWarps) * p.k) +
+                                              k + 32 * h)
+                                  : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < G; ++i) s[i] = dot8(xv[h], v[h][i], s[i]);
         }
         if (i0 + 4 >= kRanks)  // A is here: HBM's next work, behind the reductions and the barrier
             for (int64_t o = n0 * (rank * 2) + threadIdx.x * 128; o < n1 * (rank * 2); o += kRowThreads * 128)

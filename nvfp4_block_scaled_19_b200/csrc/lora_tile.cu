@@ -259,7 +259,7 @@ __device__ __forceinline__ float4 ld_cluster_16B(uint32_t a, uint32_t rank) {
 
 // ---------------------------------------------------------------- the tile's adapters
 
-struct TileSlots {
+struct alignas(16) TileSlots {
     int row[kTileRows];       // each row's adapter, as its place in `list`, or -1
     int list[kTileRows];      // the different adapters, in order of first use
     int count;
@@ -283,8 +283,16 @@ __device__ __forceinline__ void find_slots(TileSlots &ts, const nvfp4_lora_args 
     if (i < kTileRows) {
         const unsigned same = __match_any_sync(0xFFFFFFFFu, slot);
         first = slot >= 0 && lane == __ffs(same) - 1;
-        if (first)
-            for (int j = 0; j < 32 * warp; ++j) first = first && ts.row[j] != slot;
+        if (first) {  // and in no earlier warp
+            const int4 *rows = reinterpret_cast<const int4 *>(ts.row);
+            bool seen = false;
+#pragma unroll 8
+            for (int j = 0; j < 8 * warp; ++j) {
+                const int4 v = rows[j];
+                seen |= v.x == slot || v.y == slot || v.z == slot || v.w == slot;
+            }
+            first = !seen;
+        }
         __syncwarp();
         firsts = __ballot_sync(0xFFFFFFFFu, first);
         if (lane == 0) ts.warp_count[warp] = __popc(firsts);
