@@ -182,35 +182,33 @@ __device__ __forceinline__ float sixth(float a) {
 }
 
 // Codes and block scales of two vectors of a thread, as quantize_vec gives them
-// for each.  The two lanes that share a block share its scale: the even one
-// computes the first vector's, the odd one the second's, one division each.
-__device__ __forceinline__ void quantize_two(const nvfp4_residual_norm_args &a, int64_t r, int vec0,
-                                             int vec1, bool second, uint4 o0, uint4 o1, uint32_t m0,
-                                             uint32_t m1, float s_enc) {
+// for each: `q0` and `q1` are where their codes go, `sf` where the word of block
+// scales goes that this thread may have to write (see sf_word).  The two lanes
+// that share a block share its scale: the even one computes the first vector's,
+// the odd one the second's, one division each.
+__device__ __forceinline__ void quantize_two(uint8_t *q0, uint8_t *q1, uint8_t *sf, bool second, uint4 o0,
+                                             uint4 o1, uint32_t m0, uint32_t m1, float s_enc) {
     const bool odd = threadIdx.x & 1;
     m0 = max(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, 1));
     m1 = max(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, 1));
-    const uint32_t sf = e4m3_encode(__fmul_rn(sixth(__uint_as_float((odd ? m1 : m0) << 16)), s_enc));
-    const float value = e4m3_decode(sf);
+    const uint32_t code = e4m3_encode(__fmul_rn(sixth(__uint_as_float((odd ? m1 : m0) << 16)), s_enc));
+    const float value = e4m3_decode(code);
     float inv = 0.0f;
     if (value != 0.0f) {
         inv = __fdiv_rn(s_enc, value);
         if (!isfinite(inv)) inv = FLT_MAX;
     }
     const float other = __shfl_xor_sync(0xFFFFFFFFu, inv, 1);
-    uint8_t *q = a.q + r * (a.cols >> 1);
-    *reinterpret_cast<uint32_t *>(q + vec0 * 4) = quantize_bf16x8(o0, odd ? other : inv);
-    if (second) *reinterpret_cast<uint32_t *>(q + vec1 * 4) = quantize_bf16x8(o1, odd ? inv : other);
+    *reinterpret_cast<uint32_t *>(q0) = quantize_bf16x8(o0, odd ? other : inv);
+    if (second) *reinterpret_cast<uint32_t *>(q1) = quantize_bf16x8(o1, odd ? inv : other);
     // Four blocks (eight lanes) a word: lane 0 of the eight gathers the first
     // vector's, lane 1 the second's.
-    const uint32_t s = odd && !second ? 0u : sf;
-    const uint32_t s1 = __shfl_down_sync(0xFFFFFFFFu, s, 2);
-    const uint32_t s2 = __shfl_down_sync(0xFFFFFFFFu, s, 4);
-    const uint32_t s3 = __shfl_down_sync(0xFFFFFFFFu, s, 6);
-    const int vec = odd ? vec1 - 1 : vec0;
+    const uint32_t s0 = odd && !second ? 0u : code;
+    const uint32_t s1 = __shfl_down_sync(0xFFFFFFFFu, s0, 2);
+    const uint32_t s2 = __shfl_down_sync(0xFFFFFFFFu, s0, 4);
+    const uint32_t s3 = __shfl_down_sync(0xFFFFFFFFu, s0, 6);
     if ((threadIdx.x & 6) == 0 && (!odd || second))
-        *reinterpret_cast<uint32_t *>(a.sf + sf_offset(r, int64_t(vec >> 1), (a.cols + 63) >> 6)) =
-            s | (s1 << 8) | (s2 << 16) | (s3 << 24);
+        *reinterpret_cast<uint32_t *>(sf) = s0 | (s1 << 8) | (s2 << 16) | (s3 << 24);
 }
 
 // T threads per row, V vectors of 8 elements per thread (vector i of thread t
@@ -463,7 +461,7 @@ constexpr int kVecs = 2;  // vectors of 8 columns per thread
 // shared by 32 columns per thread, and the arithmetic takes fp32 pairs.
 template <bool kFull, bool kQuant, bool kStreamF32, bool kVecF32>
 __global__ void __launch_bounds__(512, 2)
-    residual_norm_rows_kernel(const nvfp4_residual_norm_args a, const int64_t rows_per_group,
+    residual_norm_rows_kernel(const nvfp4_residual_norm_args a, const uint32_t per_group,
                               const int stages, int *err) {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ __align__(8) uint64_t bars[kMaxStages];
@@ -485,7 +483,6 @@ __global__ void __launch_bounds__(512, 2)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (tx < 32) red[tx >> 4][tx & 15] = 0.0f;  // the entries past the last warp stay 0
-    __syncthreads();
 
     auto fetch = [&](int64_t r, int slot) __attribute__((always_inline)) {
         const uint32_t bar = bar_a + 8 * slot, dst = ring_a + slot * slot_bytes;
@@ -504,8 +501,12 @@ __global__ void __launch_bounds__(512, 2)
         __syncthreads();
         const float4 *b = reinterpret_cast<const float4 *>(red[turn]);
         turn ^= 1;
-        v = op(op(b[0].x, b[0].y), op(b[0].z, b[0].w));
-        for (int w = 4; w < T >> 5; w += 4) v = op(v, op(op(b[w >> 2].x, b[w >> 2].y), op(b[w >> 2].z, b[w >> 2].w)));
+        const float4 u = b[0], w = b[1];
+        v = op(op(op(u.x, u.y), op(u.z, u.w)), op(op(w.x, w.y), op(w.z, w.w)));
+        if (T > 256) {
+            const float4 y = b[2], z = b[3];
+            v = op(v, op(op(op(y.x, y.y), op(y.z, y.w)), op(op(z.x, z.y), op(z.z, z.w))));
+        }
         return v;
     };
     auto add = [](float u, float v) __attribute__((always_inline)) { return u + v; };
@@ -536,7 +537,8 @@ __global__ void __launch_bounds__(512, 2)
         return rsqrtf(fmaf(reduce(s2.x + s2.y, add), inv_cols, eps));
     };
     auto group_of = [&](int64_t r) __attribute__((always_inline)) {
-        return a.row_group != nullptr ? int64_t(__ldg(a.row_group + r)) : r / rows_per_group;
+        return a.row_group != nullptr ? int64_t(__ldg(a.row_group + r))
+                                      : int64_t(static_cast<uint32_t>(r) / per_group);
     };
     // x <- x * vector (or x + vector) where there is one.
     auto times = [&](float2 (&x)[V][4], const void *p) __attribute__((always_inline)) {
@@ -575,6 +577,7 @@ __global__ void __launch_bounds__(512, 2)
     if (tx == 0)
         for (; issued < stages && r + issued * step < a.rows; ++issued)
             fetch(r + issued * step, static_cast<int>(issued));
+    __syncthreads();
     int64_t next = r < a.rows ? group_of(r) : -1;
     int slot = 0;
     uint32_t parity = 0;
@@ -582,7 +585,12 @@ __global__ void __launch_bounds__(512, 2)
     uint8_t *hp = static_cast<uint8_t *>(a.h) + (r * a.h_stride + tx * 8) * (kStreamF32 ? 4 : 2);
     uint8_t *op = static_cast<uint8_t *>(a.out) + (r * a.out_stride + tx * 8) * 2;
     const int64_t h_step = step * a.h_stride * (kStreamF32 ? 4 : 2), o_step = step * a.out_stride * 2;
-    for (; r < a.rows; r += step, hp += h_step, op += o_step) {
+    // Of the codes; and the word of block scales that the thread may write (the
+    // first vector's for an even one, the second's for an odd one), in row 0.
+    uint8_t *qp = a.q + r * (a.cols >> 1) + tx * 4;
+    const int64_t q_step = step * (a.cols >> 1), sf_step = ((a.cols + 63) >> 6) * 512;
+    uint8_t *sf_word = a.sf + ((tx & 1 ? T + tx - 1 : tx) >> 3) * 512;
+    for (; r < a.rows; r += step, hp += h_step, op += o_step, qp += q_step) {
         const int64_t group = next;
         if (r + step < a.rows) next = group_of(r + step);
         const bool live = group >= 0 && group < a.groups;
@@ -622,7 +630,13 @@ __global__ void __launch_bounds__(512, 2)
                 times(x, a.post_weight);
                 plus(x, a.post_bias);
             }
-            const float2 rscale = both(a.residual_scale), bscale = both(a.branch_scale);
+            const float2 rscale = both(a.residual_scale);
+            if (a.branch_scale != 1.0f) {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[i][j] = __fmul2_rn(x[i][j], both(a.branch_scale));
+            }
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int vec = i * T + tx;
@@ -646,7 +660,7 @@ __global__ void __launch_bounds__(512, 2)
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    x[i][j] = __ffma2_rn(rscale, res[j], __fmul2_rn(bscale, x[i][j]));
+                    x[i][j] = __ffma2_rn(rscale, res[j], x[i][j]);
                 if (a.h != nullptr) {
                     if (kStreamF32) {
                         float4 *o = reinterpret_cast<float4 *>(hp + i * T * 32);
@@ -659,27 +673,53 @@ __global__ void __launch_bounds__(512, 2)
             }
             if (a.pre_norm != NVFP4_NORM_NONE) {
                 const float2 inv = both(centred_inverse(x, a.pre_norm, a.pre_eps));
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) x[i][j] = __fmul2_rn(x[i][j], inv);
-                times(x, a.pre_weight);
-                plus(x, a.pre_bias);
-                if (a.scale != nullptr) {
-                    const uint8_t *sp = static_cast<const uint8_t *>(a.scale) + group * a.scale_stride * vec_size;
+                const uint8_t *sp = static_cast<const uint8_t *>(a.scale) + group * a.scale_stride * vec_size;
+                const uint8_t *tp = static_cast<const uint8_t *>(a.shift) + group * a.shift_stride * vec_size;
+                if (a.pre_weight == nullptr && a.pre_bias == nullptr) {
+                    // x * (inv + inv * scale) + shift
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
                         if (i > 0 && !second) continue;
-                        RawVec<kVecF32> raw;
+                        RawVec<kVecF32> s, t;
                         float2 f[4];
-                        raw.load(sp, i * T + tx);
-                        raw.get(f);
+                        if (a.scale != nullptr) s.load(sp, i * T + tx);
+                        if (a.shift != nullptr) t.load(tp, i * T + tx);
+                        if (a.scale != nullptr) {
+                            s.get(f);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) x[i][j] = __ffma2_rn(x[i][j], f[j], x[i][j]);
+                            for (int j = 0; j < 4; ++j)
+                                x[i][j] = __fmul2_rn(x[i][j], __ffma2_rn(f[j], inv, inv));
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) x[i][j] = __fmul2_rn(x[i][j], inv);
+                        }
+                        if (a.shift != nullptr) {
+                            t.get(f);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) x[i][j] = __fadd2_rn(x[i][j], f[j]);
+                        }
                     }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) x[i][j] = __fmul2_rn(x[i][j], inv);
+                    times(x, a.pre_weight);
+                    plus(x, a.pre_bias);
+                    if (a.scale != nullptr) {
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            if (i > 0 && !second) continue;
+                            RawVec<kVecF32> raw;
+                            float2 f[4];
+                            raw.load(sp, i * T + tx);
+                            raw.get(f);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) x[i][j] = __ffma2_rn(x[i][j], f[j], x[i][j]);
+                        }
+                    }
+                    if (a.shift != nullptr) plus(x, tp);
                 }
-                if (a.shift != nullptr)
-                    plus(x, static_cast<const uint8_t *>(a.shift) + group * a.shift_stride * vec_size);
                 uint4 o[V];
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
@@ -695,7 +735,9 @@ __global__ void __launch_bounds__(512, 2)
                         a.s_dec_rows[r] = __fdiv_rn(1.0f, s_enc);
                         if (a.amax_rows != nullptr) a.amax_rows[r] = amax;
                     }
-                    quantize_two(a, r, tx, T + tx, second, o[0], o[1], m0, m1, s_enc);
+                    const uint32_t r32 = static_cast<uint32_t>(r);
+                    uint8_t *sfp = sf_word + (r >> 7) * sf_step + (r32 & 31) * 16 + ((r32 >> 5) & 3) * 4;
+                    quantize_two(qp, qp + T * 4, sfp, second, o[0], o[1], m0, m1, s_enc);
                 }
             }
         }
@@ -753,7 +795,7 @@ cudaError_t launch_rows_as(const nvfp4_residual_norm_args &a, int num_sms, cudaS
     if (e != cudaSuccess) return e;
     const int64_t grid = static_cast<int64_t>(num_sms) * per_sm;
     kernel<<<static_cast<unsigned>(grid < a.rows ? grid : a.rows), threads, smem, stream>>>(
-        a, (a.rows + a.groups - 1) / a.groups, static_cast<int>(stages), err);
+        a, static_cast<uint32_t>((a.rows + a.groups - 1) / a.groups), static_cast<int>(stages), err);
     return cudaGetLastError();
 }
 
