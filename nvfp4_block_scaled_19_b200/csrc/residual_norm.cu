@@ -470,7 +470,10 @@ __global__ void __launch_bounds__(512, 2)
     constexpr int V = kVecs;
     const int T = blockDim.x, tx = threadIdx.x, lane = tx & 31, warp = tx >> 5;
     const int nvec = static_cast<int>(a.cols) >> 3;
-    const bool second = kFull || T + tx < nvec;  // the first vector is always in the row
+    // The first vector is always in the row.  Where the second is not, its place
+    // holds the row's last one, made zero wherever it would count.
+    const bool second = kFull || T + tx < nvec;
+    const int place[V] = {tx, kFull ? T + tx : min(T + tx, nvec - 1)};
     const float inv_cols = 1.0f / static_cast<float>(a.cols);
     const uint32_t y_bytes = a.y != nullptr ? static_cast<uint32_t>(a.cols) * 2 : 0;
     const uint32_t slot_bytes = y_bytes + static_cast<uint32_t>(a.cols) * (kStreamF32 ? 4 : 2);
@@ -513,6 +516,11 @@ __global__ void __launch_bounds__(512, 2)
     auto larger = [](float u, float v) __attribute__((always_inline)) {
         return __uint_as_float(::max(__float_as_uint(u), __float_as_uint(v)));
     };
+    auto only_in_row = [&](float2 (&v)[4]) __attribute__((always_inline)) {
+        if (!kFull)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = make_float2(second ? v[j].x : 0.0f, second ? v[j].y : 0.0f);
+    };
     // x <- x - mean for a layer norm; returns 1 / sqrt(mean(x^2) + eps).
     auto centred_inverse = [&](float2 (&x)[V][4], int kind, float eps) __attribute__((always_inline)) {
         if (kind == NVFP4_NORM_LAYER) {
@@ -524,10 +532,9 @@ __global__ void __launch_bounds__(512, 2)
             const float2 mean = both(-reduce(s.x + s.y, add) * inv_cols);
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if (i == 0 || second) {  // the others stay zero
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) x[i][j] = __fadd2_rn(x[i][j], mean);
-                }
+                for (int j = 0; j < 4; ++j) x[i][j] = __fadd2_rn(x[i][j], mean);
+            only_in_row(x[1]);
         }
         float2 s2 = both(0.0f);
 #pragma unroll
@@ -546,10 +553,9 @@ __global__ void __launch_bounds__(512, 2)
         RawVec<kVecF32> raw[V];
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (i == 0 || second) raw[i].load(p, i * T + tx);
+            raw[i].load(p, place[i]);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            if (i > 0 && !second) continue;
             float2 f[4];
             raw[i].get(f);
 #pragma unroll
@@ -561,10 +567,9 @@ __global__ void __launch_bounds__(512, 2)
         RawVec<kVecF32> raw[V];
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (i == 0 || second) raw[i].load(p, i * T + tx);
+            raw[i].load(p, place[i]);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            if (i > 0 && !second) continue;
             float2 f[4];
             raw[i].get(f);
 #pragma unroll
@@ -599,19 +604,12 @@ __global__ void __launch_bounds__(512, 2)
         uint4 yv[V], rv[kStreamF32 ? 2 * V : V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int vec = i * T + tx;
-            if (!kFull && i > 0) {
-                yv[i] = rv[i] = make_uint4(0, 0, 0, 0);
-                if (kStreamF32) rv[(kStreamF32 ? V : 0) + i] = make_uint4(0, 0, 0, 0);
-            }
-            if (i == 0 || second) {
-                yv[i] = y_bytes ? lds_16B(ys + vec * 16) : make_uint4(0, 0, 0, 0);
-                if (kStreamF32) {
-                    rv[i] = lds_16B(rs + vec * 32);
-                    rv[(kStreamF32 ? V : 0) + i] = lds_16B(rs + vec * 32 + 16);
-                } else {
-                    rv[i] = lds_16B(rs + vec * 16);
-                }
+            yv[i] = y_bytes ? lds_16B(ys + place[i] * 16) : make_uint4(0, 0, 0, 0);
+            if (kStreamF32) {
+                rv[i] = lds_16B(rs + place[i] * 32);
+                rv[(kStreamF32 ? V : 0) + i] = lds_16B(rs + place[i] * 32 + 16);
+            } else {
+                rv[i] = lds_16B(rs + place[i] * 16);
             }
         }
         // The slot is free once every thread has read it: at the row's first
@@ -621,6 +619,7 @@ __global__ void __launch_bounds__(512, 2)
             float2 x[V][4];
 #pragma unroll
             for (int i = 0; i < V; ++i) unpack4(yv[i], x[i]);
+            only_in_row(x[1]);
             if (a.post_norm != NVFP4_NORM_NONE) {
                 const float2 inv = both(centred_inverse(x, a.post_norm, a.post_eps));
 #pragma unroll
@@ -639,8 +638,6 @@ __global__ void __launch_bounds__(512, 2)
             }
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const int vec = i * T + tx;
-                if (i > 0 && !second) continue;
                 float2 res[4], gf[4];
                 if (kStreamF32) {
                     const uint4 lo = rv[i], hi = rv[(kStreamF32 ? V : 0) + i];
@@ -653,7 +650,7 @@ __global__ void __launch_bounds__(512, 2)
                 }
                 if (a.gate != nullptr) {
                     RawVec<kVecF32> gate;
-                    gate.load(static_cast<const uint8_t *>(a.gate) + group * a.gate_stride * vec_size, vec);
+                    gate.load(static_cast<const uint8_t *>(a.gate) + group * a.gate_stride * vec_size, place[i]);
                     gate.get(gf);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) x[i][j] = __fmul2_rn(x[i][j], gf[j]);
@@ -661,7 +658,7 @@ __global__ void __launch_bounds__(512, 2)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     x[i][j] = __ffma2_rn(rscale, res[j], x[i][j]);
-                if (a.h != nullptr) {
+                if (a.h != nullptr && (i == 0 || second)) {
                     if (kStreamF32) {
                         float4 *o = reinterpret_cast<float4 *>(hp + i * T * 32);
                         o[0] = make_float4(x[i][0].x, x[i][0].y, x[i][1].x, x[i][1].y);
@@ -671,6 +668,7 @@ __global__ void __launch_bounds__(512, 2)
                     }
                 }
             }
+            only_in_row(x[1]);
             if (a.pre_norm != NVFP4_NORM_NONE) {
                 const float2 inv = both(centred_inverse(x, a.pre_norm, a.pre_eps));
                 const uint8_t *sp = static_cast<const uint8_t *>(a.scale) + group * a.scale_stride * vec_size;
@@ -679,11 +677,10 @@ __global__ void __launch_bounds__(512, 2)
                     // x * (inv + inv * scale) + shift
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        if (i > 0 && !second) continue;
                         RawVec<kVecF32> s, t;
                         float2 f[4];
-                        if (a.scale != nullptr) s.load(sp, i * T + tx);
-                        if (a.shift != nullptr) t.load(tp, i * T + tx);
+                        if (a.scale != nullptr) s.load(sp, place[i]);
+                        if (a.shift != nullptr) t.load(tp, place[i]);
                         if (a.scale != nullptr) {
                             s.get(f);
 #pragma unroll
@@ -709,10 +706,9 @@ __global__ void __launch_bounds__(512, 2)
                     if (a.scale != nullptr) {
 #pragma unroll
                         for (int i = 0; i < V; ++i) {
-                            if (i > 0 && !second) continue;
                             RawVec<kVecF32> raw;
                             float2 f[4];
-                            raw.load(sp, i * T + tx);
+                            raw.load(sp, place[i]);
                             raw.get(f);
 #pragma unroll
                             for (int j = 0; j < 4; ++j) x[i][j] = __ffma2_rn(x[i][j], f[j], x[i][j]);
@@ -723,7 +719,8 @@ __global__ void __launch_bounds__(512, 2)
                 uint4 o[V];
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    o[i] = pack4(x[i]);  // zero past the row
+                    o[i] = pack4(x[i]);
+                    if (!kFull && i > 0 && !second) o[i] = make_uint4(0, 0, 0, 0);
                     if (a.out != nullptr && (i == 0 || second))
                         *reinterpret_cast<uint4 *>(op + i * T * 16) = o[i];
                 }
