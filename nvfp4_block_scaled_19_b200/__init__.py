@@ -567,7 +567,9 @@ def residual_norm(residual: torch.Tensor, y: torch.Tensor | None = None, *,
     gate, scale, shift: [cols], or [groups, cols] with any row stride that is a
     multiple of 8 (chunks of one modulation tensor).  row_group: int32 per row,
     its request; rows with a negative number, or one not below groups where a
-    vector has groups, are padding, and their results are left as they were.
+    vector has groups, are padding, and their results are left as they were (in
+    tensors that the call makes, whatever the memory held: give zeroed ones where
+    a per-tensor quantize or the like will see those rows).
     Without it each request has rows / groups consecutive rows.  Weights, biases, gate, scale and shift are all bf16 or
     all fp32.  h, out and quant may be given; h may be the residual itself.
     Without pre, only h is computed."""
