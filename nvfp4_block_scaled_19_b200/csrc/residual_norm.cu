@@ -612,9 +612,19 @@ __global__ void __launch_bounds__(512, 2)
                 rv[i] = lds_16B(rs + place[i] * 16);
             }
         }
-        // The slot is free once every thread has read it: at the row's first
-        // reduction, or here where none is sure to come.
-        if (!live || (a.post_norm == NVFP4_NORM_NONE && a.pre_norm == NVFP4_NORM_NONE)) __syncthreads();
+        // The slot is free, and asked to hold a later row, once every thread has
+        // read it: at the row's first reduction, or here where none comes.
+        const bool abandoned = *static_cast<volatile int *>(&abort_flag);
+        auto refill = [&]() __attribute__((always_inline)) {
+            if (tx == 0 && r + stages * step < a.rows && !abandoned) {
+                fetch(r + stages * step, slot);
+                ++issued;
+            }
+        };
+        if (!live || (a.post_norm == NVFP4_NORM_NONE && a.pre_norm == NVFP4_NORM_NONE)) {
+            __syncthreads();
+            refill();
+        }
         if (live) {
             float2 x[V][4];
 #pragma unroll
@@ -622,6 +632,7 @@ __global__ void __launch_bounds__(512, 2)
             only_in_row(x[1]);
             if (a.post_norm != NVFP4_NORM_NONE) {
                 const float2 inv = both(centred_inverse(x, a.post_norm, a.post_eps));
+                refill();
 #pragma unroll
                 for (int i = 0; i < V; ++i)
 #pragma unroll
@@ -671,6 +682,7 @@ __global__ void __launch_bounds__(512, 2)
             only_in_row(x[1]);
             if (a.pre_norm != NVFP4_NORM_NONE) {
                 const float2 inv = both(centred_inverse(x, a.pre_norm, a.pre_eps));
+                if (a.post_norm == NVFP4_NORM_NONE) refill();
                 const uint8_t *sp = static_cast<const uint8_t *>(a.scale) + group * a.scale_stride * vec_size;
                 const uint8_t *tp = static_cast<const uint8_t *>(a.shift) + group * a.shift_stride * vec_size;
                 if (a.pre_weight == nullptr && a.pre_bias == nullptr) {
@@ -737,10 +749,6 @@ __global__ void __launch_bounds__(512, 2)
                     quantize_two(qp, qp + T * 4, sfp, second, o[0], o[1], m0, m1, s_enc);
                 }
             }
-        }
-        if (tx == 0 && r + stages * step < a.rows && !*static_cast<volatile int *>(&abort_flag)) {
-            fetch(r + stages * step, slot);
-            ++issued;
         }
         if (++slot == stages) {
             slot = 0;
