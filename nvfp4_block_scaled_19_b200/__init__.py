@@ -149,8 +149,11 @@ def _check(fn: str, status: int) -> None:
 
 
 def _stream(stream=None) -> int:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    """The given stream's handle, or that of the current device's current stream
+    (asked for by its handle: building a Stream object costs several us a call)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:
