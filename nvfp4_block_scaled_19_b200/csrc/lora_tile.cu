@@ -29,8 +29,8 @@
 //
 // Roles of both: the first and last warp TMA producers (x or y; the adapters:
 // a copy costs the thread that issues it a few hundred cycles), warp 1 MMA
-// issuer, the warps between epilogue (one 32-lane quadrant each, four for every
-// 64 columns).  Every wait is bounded; on a
+// issuer, the warps between epilogue (one 32-lane quadrant each; in the expand
+// two to a quadrant, for half a unit's columns each).  Every wait is bounded; on a
 // timeout the kernel records NVFP4_ERR_TIMEOUT (tags 40-47), all roles stop,
 // copies and MMAs in flight are drained with bounded waits and tensor memory is
 // freed.
@@ -212,12 +212,21 @@ __device__ __forceinline__ void tmem_ld_up_to_64(uint32_t addr, uint32_t (&r)[64
     for (int i = 0; i < 64; ++i) asm volatile("" : "+r"(r[i]));
 }
 
-// 64 columns of this warp's 32 lanes, complete on return.
-__device__ __forceinline__ void tmem_ld64(uint32_t addr, uint32_t (&r)[64]) {
+// 64 or 32 columns of this warp's 32 lanes, complete on return.
+__device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t (&r)[64]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(addr)
         : "memory");
 }
@@ -656,7 +665,8 @@ constexpr int kUnitsPerCta = 32;
 
 int expand_unit(int64_t rank) { return rank <= 64 ? 64 : 128; }
 
-constexpr int expand_threads(int unit) { return 32 * (3 + unit / 16); }
+constexpr int kExpandEpiWarps = 8;
+constexpr int kExpandThreads = 32 * (3 + kExpandEpiWarps);
 
 ExpandPlan expand_plan(int64_t rank) {
     const TLayout tl(static_cast<int>(rank));
@@ -675,13 +685,14 @@ ExpandPlan expand_plan(int64_t rank) {
 // The launch's units, row tile by row tile, are dealt out evenly: CTA i of G
 // takes those from units * i / G on, which are parts of one or a few tiles.
 template <int kUnit>
-__global__ void __launch_bounds__(expand_threads(kUnit))
+__global__ void __launch_bounds__(kExpandThreads, kUnit == 64 ? 2 : 1)
     lora_expand_kernel(const __grid_constant__ ExpandMaps maps, const nvfp4_lora_args p,
                        const ExpandPlan plan, const int most_adapters, int *err) {
     constexpr uint32_t kYBytes = kUnit / 64 * kBoxBytes;
     constexpr int kAccs = kAccCols / kUnit;
-    constexpr int kEpiWarps = kUnit / 16;  // four per 64 columns
-    constexpr int kBWarp = 2 + kEpiWarps;  // loads B
+    constexpr int kEpiWarps = kExpandEpiWarps;
+    constexpr int kCols = 4 * kUnit / kEpiWarps;  // columns of an epilogue warp: 32 or 64
+    constexpr int kBWarp = 2 + kEpiWarps;         // loads B
     extern __shared__ uint8_t smem_raw[];
     __shared__ TileSlots ts;
     __shared__ __align__(8) uint64_t bars[2 * kMaxYSlots + 2 * kMaxBSlots + 2 * kAccs + 2];
@@ -703,7 +714,7 @@ __global__ void __launch_bounds__(expand_threads(kUnit))
     if (threadIdx.x == 0) {
         for (int s = 0; s < plan.y_slots; ++s) {
             bar_init(y_full + 8 * s, 1);
-            bar_init(y_empty + 8 * s, kEpiWarps);
+            bar_init(y_empty + 8 * s, kUnit / 16);  // the stores of a unit
         }
         for (int s = 0; s < plan.b_slots; ++s) {
             bar_init(b_full + 8 * s, 1);
@@ -827,13 +838,19 @@ __global__ void __launch_bounds__(expand_threads(kUnit))
             }
             __syncwarp();
         } else {
-            const int quad = warp & 3, row = quad * 32 + lane, h = (warp - 2) / 4 * 64;
+            const int quad = warp & 3, row = quad * 32 + lane, first = (warp - 2) / 4 * kCols;
+            const int h = first & ~63;  // the 64-column box of its columns
+            const bool storer = (first & 63) == 0;
             const int mine = ts.row[row];
             const uint32_t swz = (row & 7) << 4;
+            const uint32_t col_bytes = (first & 63) * 2;
             const bool stored = m0 + quad * 32 < p.rows;  // a box of this warp's rows
             bool ok = true;
             for (int u = u0; u < u1; ++u) {
-                if (!bar_wait_warp(y_full + 8 * ys, yph, ab, 47)) break;
+                if (!bar_wait_warp(y_full + 8 * ys, yph, ab, 47)) {
+                    ok = false;
+                    break;
+                }
                 const uint32_t box = y_ring + ys * kYBytes + h * (kTileRows * 2);
                 for (int d = 0; d < count; ++d) {
                     if (!bar_wait_warp(d_full + 8 * acc, aph, ab, 47)) {
@@ -843,15 +860,15 @@ __global__ void __launch_bounds__(expand_threads(kUnit))
                     fence_after();
                     const uint32_t src = tmem + acc * kUnit + (static_cast<uint32_t>(quad * 32) << 16);
                     const bool any = count == 1 || __any_sync(0xFFFFFFFFu, mine == d);  // rows of it
-                    uint32_t f[64];
-                    if (any) tmem_ld64(src + h, f);
+                    uint32_t f[kCols];
+                    if (any) tmem_ld_cols(src + first, f);
                     fence_before();  // read: back to the MMA thread
                     __syncwarp();
                     if (lane == 0) bar_arrive(d_empty + 8 * acc);
                     if (mine == d) {
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const uint32_t at = box + row * 128 + ((16 * c) ^ swz);
+                        for (int c = 0; c < kCols / 8; ++c) {
+                            const uint32_t at = box + row * 128 + ((col_bytes + 16 * c) ^ swz);
                             uint4 v = ld_shared_16B(at);
                             v.x = add_pair(v.x, f[8 * c], f[8 * c + 1]);
                             v.y = add_pair(v.y, f[8 * c + 2], f[8 * c + 3]);
@@ -867,11 +884,22 @@ __global__ void __launch_bounds__(expand_threads(kUnit))
                     }
                 }
                 if (!ok) break;
-                // This warp's 32 rows go out; the slot of the unit before is free
-                // once its store has read it.
+                // A box of 32 rows and 64 columns goes out, by the warp of its first
+                // columns; the slot of the unit before is free once its store has
+                // read it.
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) {
+                if (kCols == 32) {
+                    // The two warps of a box meet.  One that gives up says so first
+                    // and arrives below, so the other is not left waiting.
+                    if (__shfl_sync(0xFFFFFFFFu, *ab.flag, 0)) {
+                        ok = false;
+                        break;
+                    }
+                    asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
+                } else {
+                    __syncwarp();
+                }
+                if (lane == 0 && storer) {
                     if (stored && u * kUnit + h < p.n)
                         store_2d(&maps.out, box + quad * 4096, u * kUnit + h, static_cast<int>(m0) + quad * 32);
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
@@ -884,6 +912,7 @@ __global__ void __launch_bounds__(expand_threads(kUnit))
                     yph ^= 1;
                 }
             }
+            if (kCols == 32 && !ok) asm volatile("bar.arrive %0, 64;" ::"r"(1 + quad) : "memory");
         }
         // Every role is done with this tile (its t, its adapters), and every
         // product of it has been read.
@@ -1012,7 +1041,7 @@ cudaError_t launch_expand(const ExpandMaps &maps, const nvfp4_lora_args &p, cons
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(expand_threads(kUnit));
+    cfg.blockDim = dim3(kExpandThreads);
     cfg.dynamicSmemBytes = plan.smem_bytes;
     cfg.stream = stream;
     cfg.attrs = &attr;
