@@ -13,6 +13,9 @@
 // 18.8 us against 16.5; behind A's loads, before they arrive, 17.6).
 // What bounds it: the adapters' bytes, rank * (K + N) * 2 per row, from HBM
 // where rows have adapters of their own and from L2 where they share them.
+// Measured: one row, rank 16, 4096 x 4096 3.5 us; 61 rows with 61 adapters of rank
+// 32, K 4096, N 12288 14.9 us (67 MB, 4.5 TB/s: 7 us until A is summed up, then B at
+// 6.9 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
