@@ -687,9 +687,92 @@ ExpandPlan expand_plan(int64_t rank) {
     return e;
 }
 
-// The launch's units, row tile by row tile, are dealt out evenly: CTA i of G
-// takes those from units * i / G on, which are parts of one or a few tiles.
-template <int kUnit>
+// The launch's units, row tile by row tile, are dealt out evenly: each CTA takes
+// a run of them, parts of one or a few tiles.  Where there are few tiles the
+// shares are weighed, as a tile with rows of several adapters takes longer: a
+// unit costs 10 with one adapter and 7 more for each other (1.6 and 2.7 us
+// measured).  Weighing takes about 2 us before a CTA's first copies: with 8 units
+// per CTA it pays (4608 rows, rank 128, three adapters 63.7 -> 61.7 us), with 3 it
+// does not (1337 rows of six requests 26.6 -> 28.6).
+constexpr int kWeighedTiles = 128, kWeighedUnits = 6;
+
+// The tiles' costs, and where two places in their sum are.
+struct Shares {
+    int prefix[kWeighedTiles + 1];  // unit costs of the tiles before each
+    long long first, last;          // this CTA's units, counted through the tiles
+};
+
+// Fills `sh` for CTA i of n (all threads call; ends with a barrier).  The
+// adapters of a tile are counted as runs of equal slots, which is exact where
+// requests are contiguous and an upper bound else.  A unit of tile t starts at
+// units * prefix[t] and its unit cost apart; a CTA's units are those that start
+// in its n-th of the sum.
+__device__ __forceinline__ void share_out(Shares &sh, const nvfp4_lora_args &p, int tiles, int units,
+                                          unsigned i, unsigned n) {
+    constexpr int kBatch = 4;  // tiles of a warp at a time, their slots loaded together
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    for (int t0 = threadIdx.x >> 5; t0 < tiles; t0 += kBatch * warps) {
+        int slot[kBatch][4];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int64_t row = int64_t(t0 + b * warps) * kTileRows + 32 * q + lane;
+                slot[b][q] = row < p.rows ? __ldg(p.row_slot + row) : -1;
+            }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int t = t0 + b * warps;
+            int runs = 0, before = -1;  // `before`: the slot of the row before these
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int s = slot[b][q] >= 0 && slot[b][q] < p.slots ? slot[b][q] : -1;
+                int left = __shfl_up_sync(0xFFFFFFFFu, s, 1);
+                if (lane == 0) left = before;
+                runs += __popc(__ballot_sync(0xFFFFFFFFu, s >= 0 && s != left));
+                before = __shfl_sync(0xFFFFFFFFu, s, 31);
+            }
+            const int most = p.slots < runs ? static_cast<int>(p.slots) : runs;
+            if (lane == 0 && t < tiles) sh.prefix[t + 1] = most > 0 ? 3 + 7 * most : p.out == p.y ? 0 : 8;
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {  // four tiles per lane
+        int c[4], sum = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int t = 4 * lane + k;
+            sum += t < tiles ? sh.prefix[t + 1] : 0;
+            c[k] = sum;
+        }
+        int upto = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+            if (lane >= o) upto += v;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (4 * lane + k < tiles) sh.prefix[4 * lane + k + 1] = upto - sum + c[k];
+        if (lane == 0) {
+            sh.prefix[0] = 0;
+            sh.first = sh.last = static_cast<long long>(tiles) * units;  // unless found below
+        }
+    }
+    __syncthreads();
+    const int t = threadIdx.x;
+    if (t < tiles) {
+        const int64_t all = int64_t(units) * sh.prefix[tiles], begin = int64_t(units) * sh.prefix[t];
+        const int cost = sh.prefix[t + 1] - sh.prefix[t];
+        const int64_t end = begin + int64_t(units) * cost;
+        const int64_t at0 = all * i / n, at1 = all * (i + 1) / n;
+        if (begin <= at0 && at0 < end) sh.first = int64_t(t) * units + (at0 - begin + cost - 1) / cost;
+        if (begin <= at1 && at1 < end) sh.last = int64_t(t) * units + (at1 - begin + cost - 1) / cost;
+    }
+    __syncthreads();
+}
+
+template <int kUnit, bool kWeighed>
 __global__ void __launch_bounds__(kExpandThreads, kUnit == 64 ? 2 : 1)
     lora_expand_kernel(const __grid_constant__ ExpandMaps maps, const nvfp4_lora_args p,
                        const ExpandPlan plan, const int most_adapters, int *err) {
@@ -714,7 +797,6 @@ __global__ void __launch_bounds__(kExpandThreads, kUnit == 64 ? 2 : 1)
     const int rank = static_cast<int>(p.rank);
     const int units = static_cast<int>((p.n + kUnit - 1) / kUnit);  // of a row tile
     const int64_t tiles = (p.rows + kTileRows - 1) / kTileRows, total = tiles * units;
-    const int64_t g0 = total * blockIdx.x / gridDim.x, g1 = total * (blockIdx.x + 1) / gridDim.x;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < plan.y_slots; ++s) {
@@ -745,6 +827,14 @@ __global__ void __launch_bounds__(kExpandThreads, kUnit == 64 ? 2 : 1)
     __syncthreads();
     fence_after();
     const uint32_t tmem = tmem_holder;
+
+    int64_t g0 = total * blockIdx.x / gridDim.x, g1 = total * (blockIdx.x + 1) / gridDim.x;
+    if (kWeighed) {
+        __shared__ Shares shares;
+        share_out(shares, p, static_cast<int>(tiles), units, blockIdx.x, gridDim.x);
+        g0 = shares.first;
+        g1 = shares.last;
+    }
 
     // Ring positions, of whichever role the thread has; they go on from tile
     // to tile.
@@ -1036,11 +1126,13 @@ int shrink_splits(int64_t rows, int64_t k) {
 template <int kUnit>
 cudaError_t launch_expand(const ExpandMaps &maps, const nvfp4_lora_args &p, const ExpandPlan &plan,
                           int64_t at_once, int most_adapters, int *err, cudaStream_t stream) {
-    const cudaError_t e = allow_smem(lora_expand_kernel<kUnit>, plan.smem_bytes);
-    if (e != cudaSuccess) return e;
-    const int64_t units = row_tiles(p.rows) * ((p.n + kUnit - 1) / kUnit);
+    const int64_t tiles = row_tiles(p.rows), units = tiles * ((p.n + kUnit - 1) / kUnit);
     const int64_t chunks = units / kUnitsPerCta;
     const int64_t grid = units < at_once ? units : chunks > at_once ? chunks : at_once;
+    const bool weighed = tiles <= kWeighedTiles && units >= kWeighedUnits * grid && p.row_slot != nullptr;
+    auto *kernel = weighed ? lora_expand_kernel<kUnit, true> : lora_expand_kernel<kUnit, false>;
+    const cudaError_t e = allow_smem(kernel, plan.smem_bytes);
+    if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
@@ -1051,7 +1143,7 @@ cudaError_t launch_expand(const ExpandMaps &maps, const nvfp4_lora_args &p, cons
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, lora_expand_kernel<kUnit>, maps, p, plan, most_adapters, err);
+    return cudaLaunchKernelEx(&cfg, kernel, maps, p, plan, most_adapters, err);
 }
 
 // Room for every split's fp32 sums: splits times the row tiles are at most an SM

@@ -87,6 +87,29 @@ def test_crowded_tiles_beside_others(nv, rank, in_place):
         assert_close(nv.lora(x, y, ad, slot, out=y), want, err)
 
 
+@pytest.mark.parametrize("rank", [16, 80])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_tiles_of_unlike_cost(nv, rank, in_place):
+    """Many columns and few row tiles, whose shares are weighed by their adapters:
+    tiles of one, of several, of none, in any order, and a short last one."""
+    rows, n, slots = 3000, 12296, 6
+    x, y, ad, any_order = _inputs(nv, rows, 192, n, rank, slots)
+    ragged = torch.full((rows,), 3, dtype=torch.int32, device="cuda")
+    ragged[100:900] = -1                      # six whole tiles without an adapter
+    ragged[900:1500] = torch.arange(600, device="cuda", dtype=torch.int32) // 50 % 6
+    ragged[2500:] = 5
+    none_at_ends = ragged.clone()
+    none_at_ends[:1024], none_at_ends[-300:] = -1, slots
+    for slot in (ragged, none_at_ends, any_order):
+        want, err = lora64(x, y, ad, slot)
+        out = y.clone() if in_place else torch.full_like(y, float("nan"))
+        nv.lora(x, out if in_place else y, ad, slot, out=out)
+        torch.cuda.synchronize()
+        code, tag = nv.device_error()
+        assert code == 0, f"device wait timed out (tag {tag})"
+        assert_close(out, want, err)
+
+
 @pytest.mark.parametrize("rows", [3, 300])
 def test_no_row_has_an_adapter(nv, rows):
     x, y, ad, slot = _inputs(nv, rows, 256, 512, 16, 2)
