@@ -181,6 +181,19 @@ __device__ __forceinline__ float sixth(float a) {
     return __fmaf_rn(__fmaf_rn(-6.0f, q, a), c, q);
 }
 
+// Value of an E4M3 code by the conversion instructions (every one is a half).
+__device__ __forceinline__ float e4m3_value(uint32_t code) {
+    float v;
+    asm("{\n\t.reg .b32 h2;\n\t.reg .b16 c, lo, hi;\n\t"
+        "cvt.u16.u32 c, %1;\n\t"
+        "cvt.rn.f16x2.e4m3x2 h2, c;\n\t"
+        "mov.b32 {lo, hi}, h2;\n\t"
+        "cvt.f32.f16 %0, lo;\n\t}\n"
+        : "=f"(v)
+        : "r"(code));
+    return v;
+}
+
 // Codes and block scales of two vectors of a thread, as quantize_vec gives them
 // for each: `q0` and `q1` are where their codes go, `sf` where the word of block
 // scales goes that this thread may have to write (see sf_word).  The two lanes
@@ -192,7 +205,7 @@ __device__ __forceinline__ void quantize_two(uint8_t *q0, uint8_t *q1, uint8_t *
     m0 = max(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, 1));
     m1 = max(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, 1));
     const uint32_t code = e4m3_encode(__fmul_rn(sixth(__uint_as_float((odd ? m1 : m0) << 16)), s_enc));
-    const float value = e4m3_decode(code);
+    const float value = e4m3_value(code);
     float inv = 0.0f;
     if (value != 0.0f) {
         inv = __fdiv_rn(s_enc, value);
@@ -503,9 +516,8 @@ __global__ void __launch_bounds__(512, 2)
                   slot_bytes - y_bytes, bar);
     };
     int turn = 0;
-    auto reduce = [&](float v, auto op) __attribute__((always_inline)) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    // `v` is the warp's already.
+    auto reduce_warps = [&](float v, auto op) __attribute__((always_inline)) {
         if (lane == 0) red[turn][warp] = v;
         __syncthreads();
         const float4 *b = reinterpret_cast<const float4 *>(red[turn]);
@@ -519,6 +531,11 @@ __global__ void __launch_bounds__(512, 2)
         return v;
     };
     auto add = [](float u, float v) __attribute__((always_inline)) { return u + v; };
+    auto sum = [&](float v) __attribute__((always_inline)) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+        return reduce_warps(v, add);
+    };
     auto larger = [](float u, float v) __attribute__((always_inline)) {
         return __uint_as_float(::max(__float_as_uint(u), __float_as_uint(v)));
     };
@@ -535,7 +552,7 @@ __global__ void __launch_bounds__(512, 2)
             for (int i = 0; i < V; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s = __fadd2_rn(s, x[i][j]);
-            const float2 mean = both(-reduce(s.x + s.y, add) * inv_cols);
+            const float2 mean = both(-sum(s.x + s.y) * inv_cols);
 #pragma unroll
             for (int i = 0; i < V; ++i)
 #pragma unroll
@@ -547,7 +564,7 @@ __global__ void __launch_bounds__(512, 2)
         for (int i = 0; i < V; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) s2 = __ffma2_rn(x[i][j], x[i][j], s2);
-        return rsqrtf(fmaf(reduce(s2.x + s2.y, add), inv_cols, eps));
+        return rsqrtf(fmaf(sum(s2.x + s2.y), inv_cols, eps));
     };
     auto group_of = [&](int64_t r) __attribute__((always_inline)) {
         return a.row_group != nullptr ? int64_t(__ldg(a.row_group + r))
@@ -744,7 +761,8 @@ __global__ void __launch_bounds__(512, 2)
                 }
                 if (kQuant) {
                     const uint32_t m0 = absmax_bf16x8(o[0]), m1 = absmax_bf16x8(o[1]);
-                    const float amax = reduce(__uint_as_float(::max(m0, m1) << 16), larger);
+                    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, ::max(m0, m1));
+                    const float amax = reduce_warps(__uint_as_float(m << 16), larger);
                     const float s_enc = tensor_encode_scale(amax);
                     if (tx == 0) {
                         a.s_dec_rows[r] = __fdiv_rn(1.0f, s_enc);
