@@ -492,8 +492,12 @@ def _row_stride(t: torch.Tensor, name: str, dtype, shape, index: int) -> int:
     return stride if shape[0] > 1 else shape[1]
 
 
+def _holds(t: torch.Tensor, dtype, count: int, index: int) -> bool:
+    return t.dtype is dtype and t.numel() == count and t.get_device() == index and t.is_contiguous()
+
+
 def _row_index(t: torch.Tensor, name: str, rows: int, index: int) -> int:
-    if t.dtype is not torch.int32 or t.get_device() != index or t.numel() != rows or not t.is_contiguous():
+    if not _holds(t, torch.int32, rows, index):
         raise ValueError(f"{name} must hold one int32 per row, on the device of the others")
     return t.data_ptr()
 
@@ -606,15 +610,16 @@ def residual_norm(residual: torch.Tensor, y: torch.Tensor | None = None, *,
         if quant is None and want_quant:
             quant = empty_nvfp4(rows, cols, residual.device, row_scales=True)
         elif quant is not None:
-            if ((quant.rows, quant.cols) != (rows, cols) or quant.s_dec.numel() != rows or
-                    quant.q.get_device() != dev or quant.q.numel() != rows * cols // 2 or
-                    quant.sf.numel() != sf_bytes(rows, cols)):
-                raise ValueError("quant must be an NVFP4Tensor of these rows and columns with row scales")
+            if not (quant.rows == rows and quant.cols == cols and
+                    _holds(quant.q, torch.uint8, rows * cols // 2, dev) and
+                    _holds(quant.sf, torch.uint8, sf_bytes(rows, cols), dev) and
+                    _holds(quant.s_dec, torch.float32, rows, dev)):
+                raise ValueError("quant must be a contiguous NVFP4Tensor of these rows and columns with "
+                                 "row scales, on the device of the others")
         if quant is not None:
             q_ptr, sf_ptr, s_dec_ptr = quant.q.data_ptr(), quant.sf.data_ptr(), quant.s_dec.data_ptr()
     if amax_rows is not None:
-        if (quant is None or amax_rows.numel() != rows or amax_rows.dtype != torch.float32 or
-                amax_rows.get_device() != dev or not amax_rows.is_contiguous()):
+        if quant is None or not _holds(amax_rows, torch.float32, rows, dev):
             raise ValueError("amax_rows must hold one fp32 per row, and needs quant")
         amax_ptr = amax_rows.data_ptr()
 

@@ -292,3 +292,16 @@ def test_refusals(nv):
         with pytest.raises(nv.NVFP4Error) as e:
             nv.residual_norm(kw.pop("residual"), kw.pop("y"), pre=pre, **kw)
         assert e.value.status == status
+
+
+@pytest.mark.parametrize("field,make", [
+    ("q", lambda t: t.cpu()), ("q", lambda t: t.float()), ("q", lambda t: t.t().contiguous().t()),
+    ("sf", lambda t: t.cpu()), ("sf", lambda t: t[:-1]), ("sf", lambda t: t.repeat_interleave(2)[::2]),
+    ("s_dec", lambda t: t.cpu()), ("s_dec", lambda t: t.half()), ("s_dec", lambda t: t.repeat_interleave(2)[::2]),
+])
+def test_refuses_codes_it_cannot_write(nv, field, make):
+    r = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda")
+    q = nv.empty_nvfp4(4, 64, row_scales=True)
+    setattr(q, field, make(getattr(q, field)))
+    with pytest.raises(ValueError):
+        nv.residual_norm(r, r, pre=nv.Norm(), quant=q)
