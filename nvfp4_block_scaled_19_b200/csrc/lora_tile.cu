@@ -2,7 +2,8 @@
 // launches on 128-row tiles, both tcgen05 with TMA-fed shared memory.
 //
 // lora_shrink_kernel   t[m] = scale[s] * A[s] x[m].
-//   A cluster of `splits` CTAs per row tile, each over its share of K.  A stage
+//   A cluster of `splits` CTAs per row tile, each over its share of K (where there
+//   are few tiles, several clusters, each for a part of the tile's adapters).  A stage
 //   is the tile's 128 x 64 piece of x and, side by side as one B operand, the
 //   matching rank x 64 pieces of up to G = 256 / rank different adapters, so a
 //   tile whose rows belong to G requests still reads x once; each row's
@@ -377,8 +378,8 @@ constexpr int kMaxSlots = 8;
 
 __global__ void __launch_bounds__(kThreads)
     lora_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const nvfp4_lora_args p,
-                       const int splits, const uint32_t ring_bytes, const int most_adapters,
-                       int *crowded, float *partial, uint16_t *t, int *err) {
+                       const int splits, const int parts, const uint32_t ring_bytes,
+                       const int most_adapters, int *crowded, float *partial, uint16_t *t, int *err) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ TileSlots ts;
     __shared__ float scales[kTileRows];
@@ -390,7 +391,8 @@ __global__ void __launch_bounds__(kThreads)
     const uint32_t acc_full = empty + 8 * kMaxSlots, acc_empty = acc_full + 8, drain = acc_empty + 8;
     const Abort ab{&abort_flag, err};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tile = blockIdx.x / splits, split = blockIdx.x % splits;
+    const int tile = blockIdx.x / (splits * parts), split = blockIdx.x % splits;
+    const int part = blockIdx.x / splits % parts;
     const int64_t m0 = int64_t(tile) * kTileRows;
     const int rank = static_cast<int>(p.rank);
     const int k_blocks = static_cast<int>((p.k + 63) / 64);
@@ -429,8 +431,10 @@ __global__ void __launch_bounds__(kThreads)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tmem = tmem_holder;
     // A crowded tile is left to the kernel of single rows.
-    const int count = ts.count <= most_adapters ? ts.count : 0;
-    if (split == 0 && threadIdx.x == 64) crowded[tile] = ts.count > most_adapters;
+    const int all = ts.count <= most_adapters ? ts.count : 0;
+    if (split == 0 && part == 0 && threadIdx.x == 64) crowded[tile] = ts.count > most_adapters;
+    const int begin = all * part / parts, end = all * (part + 1) / parts;  // this cluster's adapters
+    const int count = end - begin;
     const int group = max(1, min(kAccCols / rank, count));  // adapters per pass over x
     const int passes = (count + group - 1) / group;          // 0: no row has an adapter
     const uint32_t a_slot = group * rank * 128;              // at most 32 KB
@@ -481,7 +485,7 @@ __global__ void __launch_bounds__(kThreads)
             uint32_t phase = 0;
             bool ok = true;
             for (int q = 0; q < passes && ok; ++q) {
-                const int d0 = q * group, d1 = min(count, d0 + group);
+                const int d0 = begin + q * group, d1 = min(end, d0 + group);
                 for (int kb = kb0; kb < kb0 + kbs; ++kb) {
                     if (!bar_wait(empty + 8 * slot, phase ^ 1, ab, 40)) {
                         ok = false;
@@ -515,7 +519,7 @@ __global__ void __launch_bounds__(kThreads)
             uint32_t phase = 0;
             bool ok = true;
             for (int q = 0; q < passes && ok; ++q) {
-                const int d0 = q * group, d1 = min(count, d0 + group);
+                const int d0 = begin + q * group, d1 = min(end, d0 + group);
                 const uint32_t idesc = bf16_idesc((d1 - d0) * rank);
                 if (!bar_wait(acc_empty, (q & 1) ^ 1, ab, 41)) break;
                 fence_after();
@@ -547,10 +551,10 @@ __global__ void __launch_bounds__(kThreads)
         const TLayout tl(rank);
         float *dst = partial + (int64_t(split) * p.rows + m0 + row) * rank;
         uint16_t *tdst = t + (m0 + row) * (tl.groups * 64);
-        if (row < count) scales[row] = __ldg(p.scale + ts.list[row]);
+        if (row < all) scales[row] = __ldg(p.scale + ts.list[row]);
         const float c = mine >= 0 ? __ldg(p.scale + ts.list[mine]) : 0.0f;
         for (int q = 0; q < passes; ++q) {
-            const int d0 = q * group, d1 = min(count, d0 + group);
+            const int d0 = begin + q * group, d1 = min(end, d0 + group);
             if (!bar_wait_warp(acc_full, q & 1, ab, 43)) break;
             fence_after();
             const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16);
@@ -602,7 +606,7 @@ __global__ void __launch_bounds__(kThreads)
         for (int i = threadIdx.x; i < share * (rank >> 3); i += kThreads) {
             const int row = split * share + i % share, r = i / share * 8;
             const int d = row < kTileRows && passes > 0 ? ts.row[row] : -1;
-            if (d < 0) continue;
+            if (d < begin || d >= end) continue;
             float4 w[kMaxSplits][2];  // asked for together
             if (passes == 1) {
                 const uint32_t at = x_ring + ((r >> 2) * kTileRows + row) * 16;
@@ -1076,13 +1080,13 @@ cudaError_t allow_smem(K kernel, uint32_t bytes) {
                                 static_cast<int>(bytes));
 }
 
-cudaLaunchConfig_t shrink_config(int64_t tiles, int splits, uint32_t rings, cudaLaunchAttribute *attr,
+cudaLaunchConfig_t shrink_config(int64_t clusters, int splits, uint32_t rings, cudaLaunchAttribute *attr,
                                  cudaStream_t stream) {
     attr->id = cudaLaunchAttributeClusterDimension;
     attr->val.clusterDim.x = static_cast<unsigned>(splits);
     attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits));
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * splits));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = rings + 1024;
     cfg.stream = stream;
@@ -1121,6 +1125,17 @@ int shrink_splits(int64_t rows, int64_t k) {
     for (int s = kMaxSplits; s > 1; --s)
         if (blocks / s >= 4 && tiles * s <= kSms && tiles <= clusters_at_once(s)) return s;
     return 1;
+}
+
+// Clusters of a row tile, each for a part of its adapters: as many as there can be
+// adapters and as all run at once, since one cluster draws only so much of the
+// adapters (us, one part / as many: 252 rows with 20 adapters of rank 48 62 / 38;
+// 92 rows with 6 of rank 112 33 / 21; 714 rows with 1 to 5 of rank 32 a tile 30.7 /
+// 31.3).  Only as many as passes over x saved 1 to 2 us less.
+int shrink_parts(int64_t tiles, int splits, int64_t slots) {
+    if (splits == 1) return 1;
+    const int64_t most = clusters_at_once(splits) / tiles, useful = slots < kTileRows ? slots : kTileRows;
+    return static_cast<int>(most < 1 ? 1 : most < useful ? most : useful);
 }
 
 template <int kUnit>
@@ -1190,11 +1205,12 @@ cudaError_t launch_lora_tile(const nvfp4_lora_args &p, int most_adapters, const 
     if (e != cudaSuccess) return e;
     const int splits = shrink_splits(p.rows, p.k);
     const int64_t tiles = row_tiles(p.rows);
+    const int parts = shrink_parts(tiles, splits, p.slots);
     const uint32_t rings = tiles * splits <= kSms ? kLargeRings : kSmallRings;
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = shrink_config(tiles, splits, rings, &attr, stream);
-    e = cudaLaunchKernelEx(&cfg, lora_shrink_kernel, sm, p, splits, rings, most_adapters, crowded, partial, t,
-                           err);
+    const cudaLaunchConfig_t cfg = shrink_config(tiles * parts, splits, rings, &attr, stream);
+    e = cudaLaunchKernelEx(&cfg, lora_shrink_kernel, sm, p, splits, parts, rings, most_adapters, crowded, partial,
+                           t, err);
     if (e != cudaSuccess) return e;
     return expand_unit(p.rank) == 64 ? launch_expand<64>(em, p, plan, 2 * kSms, most_adapters, err, stream)
                                      : launch_expand<128>(em, p, plan, kSms, most_adapters, err, stream);

@@ -110,6 +110,26 @@ def test_tiles_of_unlike_cost(nv, rank, in_place):
         assert_close(out, want, err)
 
 
+@pytest.mark.parametrize("rank,slots,k", [(16, 40, 1040), (48, 21, 4112), (112, 7, 4096), (128, 13, 2048)])
+@pytest.mark.parametrize("rows", [92, 252, 700])
+def test_many_adapters_in_few_tiles(nv, rows, rank, slots, k):
+    """Row tiles whose adapters are dealt out to several clusters: more and fewer
+    adapters than clusters, tiles with one or none, contiguous and in any order."""
+    n = 1032
+    x, y, ad, any_order = _inputs(nv, rows, k, n, rank, slots)
+    at = torch.arange(rows, device="cuda", dtype=torch.int32)
+    runs = at * slots // rows
+    one = torch.where(at < rows // 2, -1, slots - 1).to(torch.int32)
+    for slot in (runs, one, any_order):
+        want, err = lora64(x, y, ad, slot)
+        out = torch.full_like(y, float("nan"))
+        nv.lora(x, y, ad, slot, out=out)
+        torch.cuda.synchronize()
+        code, tag = nv.device_error()
+        assert code == 0, f"device wait timed out (tag {tag})"
+        assert_close(out, want, err)
+
+
 @pytest.mark.parametrize("rows", [3, 300])
 def test_no_row_has_an_adapter(nv, rows):
     x, y, ad, slot = _inputs(nv, rows, 256, 512, 16, 2)
