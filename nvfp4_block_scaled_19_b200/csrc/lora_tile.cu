@@ -29,7 +29,7 @@
 // below tcgen05's rate.  Measured, both launches: 16896 rows, rank 16, K 4096, N
 // 12288 176 us (0.97 GB, 5.5 TB/s; 35 us of it the shrink, which shares HBM with
 // the write-back of what ran before); 4608 rows, rank 128, K 12288, N 4096, three
-// adapters 63 us (40 and 23); 1337 rows of six requests, rank 64, 5120 x 5120
+// adapters 61 us (40 and 21); 1337 rows of six requests, rank 64, 5120 x 5120
 // 24 us, most of it start-up, sums over the cluster and tiles of two or three
 // requests.
 //
