@@ -22,6 +22,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "block_ops.h"
@@ -368,6 +369,10 @@ __global__ void __launch_bounds__(T *ROWS) residual_norm_kernel(const nvfp4_resi
 
 constexpr int kMaxStages = 8;
 constexpr int kRingBytes = 160 * 1024;
+// Of a CTA: half the ring's bytes (two CTAs at least share an SM), or two rows of
+// the widest kind, 8192 columns of bf16 y and fp32 residual.
+constexpr int kMaxRowBytes = 8192 * (2 + 4);
+constexpr int kMaxSmem = 2 * kMaxRowBytes > kRingBytes / 2 ? 2 * kMaxRowBytes : kRingBytes / 2;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr int kTimeoutTag = 48;
 
@@ -819,9 +824,18 @@ cudaError_t launch_rows_as(const nvfp4_residual_norm_args &a, int num_sms, cudaS
     int64_t stages = kRingBytes / per_sm / slot;
     stages = stages < 2 ? 2 : stages > kMaxStages ? kMaxStages : stages;
     const int smem = static_cast<int>(stages * slot);
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+    // The limit belongs to the kernel, whichever host thread sets it: once per device,
+    // to the most that any width takes, or a call of narrow rows could lower it
+    // between another thread's setting and launch.
+    static std::atomic<int> configured[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!configured[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+        if (e != cudaSuccess) return e;
+        configured[dev].store(1, std::memory_order_release);
+    }
     const int64_t grid = static_cast<int64_t>(num_sms) * per_sm;
     kernel<<<static_cast<unsigned>(grid < a.rows ? grid : a.rows), threads, smem, stream>>>(
         a, static_cast<uint32_t>((a.rows + a.groups - 1) / a.groups), static_cast<int>(stages), err);
