@@ -11,6 +11,10 @@ This module only marshals arguments: every step runs in the CUDA kernels of
 libnvfp4.so through its C ABI (include/nvfp4.h).  PyTorch supplies device
 memory and the current stream.  There is no CPU fallback: if the library is
 missing or the device is not sm_100, calls raise.
+
+A call with stream= works on that stream, and the tensors it makes belong to it:
+they may be dropped at any time, and used on the caller's current stream once
+that waits for the given one; on a third stream they need record_stream.
 """
 from __future__ import annotations
 
@@ -156,6 +160,19 @@ def _stream(stream=None) -> int:
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A new tensor that a call writes on the given stream (or the current one).
+    It comes from the memory of the stream that writes it, where no other work
+    can still hold it, and is not given out again before what the caller's
+    stream has read of it by then is done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def _ptr(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
@@ -183,11 +200,11 @@ class NVFP4Tensor:
     cols: int
 
 
-def empty_nvfp4(rows: int, cols: int, device=None, row_scales: bool = False) -> NVFP4Tensor:
+def empty_nvfp4(rows: int, cols: int, device=None, row_scales: bool = False, stream=None) -> NVFP4Tensor:
     dev = torch.device("cuda") if device is None else device
-    return NVFP4Tensor(torch.empty(rows, cols // 2, dtype=torch.uint8, device=dev),
-                       torch.empty(sf_bytes(rows, cols), dtype=torch.uint8, device=dev),
-                       torch.empty(rows if row_scales else 1, dtype=torch.float32, device=dev),
+    return NVFP4Tensor(_empty((rows, cols // 2), torch.uint8, dev, stream),
+                       _empty((sf_bytes(rows, cols),), torch.uint8, dev, stream),
+                       _empty((rows if row_scales else 1,), torch.float32, dev, stream),
                        rows, cols)
 
 
@@ -195,7 +212,7 @@ def tensor_amax(x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -
     """max |x| of a bf16 CUDA tensor into a 1-element fp32 CUDA tensor."""
     _require(x, torch.bfloat16, "x")
     if out is None:
-        out = torch.empty(1, dtype=torch.float32, device=x.device)
+        out = _empty((1,), torch.float32, x.device, stream)
     _check("nvfp4_tensor_amax", lib().nvfp4_tensor_amax(x.data_ptr(), x.numel(), out.data_ptr(),
                                                         _stream(stream)))
     return out
@@ -206,7 +223,7 @@ def quantize(x: torch.Tensor, amax: torch.Tensor, out: NVFP4Tensor | None = None
     """Dynamic NVFP4 quantization of bf16 x[rows, cols] given its amax (device)."""
     _require(x, torch.bfloat16, "x")
     rows, cols = x.shape
-    out = empty_nvfp4(rows, cols, x.device) if out is None else out
+    out = empty_nvfp4(rows, cols, x.device, stream=stream) if out is None else out
     _check("nvfp4_quantize", lib().nvfp4_quantize(
         x.data_ptr(), rows, cols, amax.data_ptr(), out.q.data_ptr(), out.sf.data_ptr(),
         out.s_dec.data_ptr(), _stream(stream)))
@@ -218,7 +235,7 @@ def quantize_with_scale(x: torch.Tensor, s_enc: torch.Tensor, out: NVFP4Tensor |
     """NVFP4 quantization with a static per-tensor scale S_enc (device fp32)."""
     _require(x, torch.bfloat16, "x")
     rows, cols = x.shape
-    out = empty_nvfp4(rows, cols, x.device) if out is None else out
+    out = empty_nvfp4(rows, cols, x.device, stream=stream) if out is None else out
     _check("nvfp4_quantize_with_scale", lib().nvfp4_quantize_with_scale(
         x.data_ptr(), rows, cols, s_enc.data_ptr(), out.q.data_ptr(), out.sf.data_ptr(),
         out.s_dec.data_ptr(), _stream(stream)))
@@ -232,7 +249,7 @@ def quantize_one_pass(x: torch.Tensor, amax_prev: torch.Tensor, amax_out: torch.
     different device fp32) for the next call."""
     _require(x, torch.bfloat16, "x")
     rows, cols = x.shape
-    out = empty_nvfp4(rows, cols, x.device) if out is None else out
+    out = empty_nvfp4(rows, cols, x.device, stream=stream) if out is None else out
     _check("nvfp4_quantize_one_pass", lib().nvfp4_quantize_one_pass(
         x.data_ptr(), rows, cols, amax_prev.data_ptr(), out.q.data_ptr(), out.sf.data_ptr(),
         out.s_dec.data_ptr(), amax_out.data_ptr(), _stream(stream)))
@@ -260,7 +277,7 @@ def quantize_dynamic(x: torch.Tensor, out: NVFP4Tensor | None = None,
     """Per-call activation path in one launch: amax, S_enc, block quantize."""
     _require(x, torch.bfloat16, "x")
     rows, cols = x.shape
-    out = empty_nvfp4(rows, cols, x.device) if out is None else out
+    out = empty_nvfp4(rows, cols, x.device, stream=stream) if out is None else out
     ws = dynamic_workspace(x.device) if workspace is None else workspace
     _check("nvfp4_quantize_dynamic", lib().nvfp4_quantize_dynamic(
         x.data_ptr(), rows, cols, out.q.data_ptr(), out.sf.data_ptr(), out.s_dec.data_ptr(),
@@ -274,7 +291,7 @@ def quantize_rowwise(x: torch.Tensor, out: NVFP4Tensor | None = None,
     scale 2688 / amax(row); out.s_dec holds one decode scale per row."""
     _require(x, torch.bfloat16, "x")
     rows, cols = x.shape
-    out = empty_nvfp4(rows, cols, x.device, row_scales=True) if out is None else out
+    out = empty_nvfp4(rows, cols, x.device, True, stream) if out is None else out
     if out.s_dec.numel() != rows:
         raise ValueError("out.s_dec must hold one scale per row")
     _check("nvfp4_quantize_rowwise", lib().nvfp4_quantize_rowwise(
@@ -302,7 +319,7 @@ def gemm(a: NVFP4Tensor, b: NVFP4Tensor, y: torch.Tensor | None = None,
     if b.cols != K:
         raise ValueError("K mismatch")
     if y is None and want_y:
-        y = torch.empty(M, N, dtype=torch.bfloat16, device=a.q.device)
+        y = _empty((M, N), torch.bfloat16, a.q.device, stream)
     fo = None
     if fused is not None:
         fo = FusedOut(fused.s_enc.data_ptr(), fused.out.q.data_ptr(), fused.out.sf.data_ptr(),
@@ -338,8 +355,8 @@ def quantize_fp8(x: torch.Tensor, amax: torch.Tensor | None = None,
     rows, cols = x.shape
     amax = tensor_amax(x, stream=stream) if amax is None else amax
     if out is None:
-        out = FP8Tensor(torch.empty(rows, cols, dtype=torch.uint8, device=x.device),
-                        torch.empty(1, dtype=torch.float32, device=x.device), rows, cols)
+        out = FP8Tensor(_empty((rows, cols), torch.uint8, x.device, stream),
+                        _empty((1,), torch.float32, x.device, stream), rows, cols)
     _check("nvfp4_fp8_quantize", lib().nvfp4_fp8_quantize(
         x.data_ptr(), rows, cols, amax.data_ptr(), out.q.data_ptr(), out.s_dec.data_ptr(),
         _stream(stream)))
@@ -353,7 +370,7 @@ def gemm_fp8(a: FP8Tensor, b: FP8Tensor, y: torch.Tensor | None = None,
     if b.cols != K:
         raise ValueError("K mismatch")
     if y is None and want_y:
-        y = torch.empty(M, N, dtype=torch.bfloat16, device=a.q.device)
+        y = _empty((M, N), torch.bfloat16, a.q.device, stream)
     fo = None
     if fused is not None:
         fo = FusedOut(fused.s_enc.data_ptr(), fused.out.q.data_ptr(), fused.out.sf.data_ptr(),
@@ -592,7 +609,7 @@ def residual_norm(residual: torch.Tensor, y: torch.Tensor | None = None, *,
         y_stride = _row_stride(y, "y", bf16, shape, dev)
         y_ptr = y.data_ptr()
         if h is None and want_h:
-            h = torch.empty(rows, cols, dtype=stream_type, device=residual.device)
+            h = _empty((rows, cols), stream_type, residual.device, stream)
     elif post is not None or gate is not None or h is not None:
         raise ValueError("post, gate and h need y")
     if h is not None:
@@ -603,12 +620,12 @@ def residual_norm(residual: torch.Tensor, y: torch.Tensor | None = None, *,
             raise ValueError("scale, shift, out and quant need pre")
     else:
         if out is None and want_out:
-            out = torch.empty(rows, cols, dtype=bf16, device=residual.device)
+            out = _empty((rows, cols), bf16, residual.device, stream)
         if out is not None:
             out_stride = _row_stride(out, "out", bf16, shape, dev)
             out_ptr = out.data_ptr()
         if quant is None and want_quant:
-            quant = empty_nvfp4(rows, cols, residual.device, row_scales=True)
+            quant = empty_nvfp4(rows, cols, residual.device, True, stream)
         elif quant is not None:
             if not (quant.rows == rows and quant.cols == cols and
                     _holds(quant.q, torch.uint8, rows * cols // 2, dev) and
@@ -723,7 +740,7 @@ def lora(x: torch.Tensor, y: torch.Tensor, adapters: LoraAdapters,
     x_stride = _row_stride(x, "x", bf16, (rows, k), dev)
     y_stride = _row_stride(y, "y", bf16, (rows, n), dev)
     if out is None:
-        out = torch.empty(rows, n, dtype=bf16, device=x.device)
+        out = _empty((rows, n), bf16, x.device, stream)
     out_stride = y_stride if out is y else _row_stride(out, "out", bf16, (rows, n), dev)
     index = 0 if row_slot is None else _row_index(row_slot, "row_slot", rows, dev)
     need = lib().nvfp4_lora_workspace_bytes(rows, k, n, rank)
