@@ -173,16 +173,18 @@ __device__ __forceinline__ void quantize_vec(const nvfp4_residual_norm_args &a, 
 // without rounding; adding its sixth, computed to 24 bits, makes the value that
 // is rounded at the end agree with a / 6 to 2^-22 units, and a / 6 of a bf16 a
 // is 0, 1/3 or 2/3 of a unit above a representable number, at least 1/6 from
-// where rounding changes.  Values whose quotient could be subnormal take the
-// double product of nvfp4_math.cuh.
+// where rounding changes.  Values whose quotient could be subnormal (below 2^-100),
+// infinity and NaN take the double product of nvfp4_math.cuh.
 __device__ __forceinline__ float sixth(float a) {
-    if (a < 7.888609e-31f /* 2^-100 */) return div6_short(a);
+    constexpr uint32_t least = 27u << 23 /* 2^-100 */, inf = 0x7F800000u;
+    if (__float_as_uint(a) - least >= inf - least) return div6_short(a);
     const float c = 1.0f / 6.0f;
     const float q = __fmul_rn(a, c);
     return __fmaf_rn(__fmaf_rn(-6.0f, q, a), c, q);
 }
 
-// Value of an E4M3 code by the conversion instructions (every one is a half).
+// Value of an E4M3 code by the conversion instructions (every one is a half); of
+// NaN's code (an infinite block under S_enc = 0) 480, as e4m3_decode reads it.
 __device__ __forceinline__ float e4m3_value(uint32_t code) {
     float v;
     asm("{\n\t.reg .b32 h2;\n\t.reg .b16 c, lo, hi;\n\t"
@@ -192,7 +194,7 @@ __device__ __forceinline__ float e4m3_value(uint32_t code) {
         "cvt.f32.f16 %0, lo;\n\t}\n"
         : "=f"(v)
         : "r"(code));
-    return v;
+    return code == 0x7Fu ? 480.0f : v;
 }
 
 // Codes and block scales of two vectors of a thread, as quantize_vec gives them
