@@ -706,13 +706,13 @@ struct Shares {
     long long first, last;          // this CTA's units, counted through the tiles
 };
 
-// Fills `sh` for CTA i of n (all threads call; ends with a barrier).  The
-// adapters of a tile are counted as runs of equal slots, which is exact where
-// requests are contiguous and an upper bound else.  A unit of tile t starts at
-// units * prefix[t] and its unit cost apart; a CTA's units are those that start
-// in its n-th of the sum.
+// Fills `sh` for CTA i of n (all threads call; ends with a barrier).  A tile's cost
+// goes by its different adapters, in whatever order its rows have them; one that
+// is left to the kernel of single rows (more than most_adapters) costs nothing
+// here.  A unit of tile t starts at units * prefix[t] and its unit cost apart; a
+// CTA's units are those that start in its n-th of the sum.
 __device__ __forceinline__ void share_out(Shares &sh, const nvfp4_lora_args &p, int tiles, int units,
-                                          unsigned i, unsigned n) {
+                                          int most_adapters, unsigned i, unsigned n) {
     constexpr int kBatch = 4;  // tiles of a warp at a time, their slots loaded together
     const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     for (int t0 = threadIdx.x >> 5; t0 < tiles; t0 += kBatch * warps) {
@@ -722,22 +722,25 @@ __device__ __forceinline__ void share_out(Shares &sh, const nvfp4_lora_args &p, 
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int64_t row = int64_t(t0 + b * warps) * kTileRows + 32 * q + lane;
-                slot[b][q] = row < p.rows ? __ldg(p.row_slot + row) : -1;
+                const int s = row < p.rows ? __ldg(p.row_slot + row) : -1;
+                slot[b][q] = s >= 0 && s < p.slots ? s : -1;
             }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
+            // One adapter after the other is counted and struck out of every lane.
             const int t = t0 + b * warps;
-            int runs = 0, before = -1;  // `before`: the slot of the row before these
+            int count = 0;
+            while (count <= most_adapters) {
+                const int next = __reduce_max_sync(
+                    0xFFFFFFFFu, max(max(slot[b][0], slot[b][1]), max(slot[b][2], slot[b][3])));
+                if (next < 0) break;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int s = slot[b][q] >= 0 && slot[b][q] < p.slots ? slot[b][q] : -1;
-                int left = __shfl_up_sync(0xFFFFFFFFu, s, 1);
-                if (lane == 0) left = before;
-                runs += __popc(__ballot_sync(0xFFFFFFFFu, s >= 0 && s != left));
-                before = __shfl_sync(0xFFFFFFFFu, s, 31);
+                for (int q = 0; q < 4; ++q)
+                    if (slot[b][q] == next) slot[b][q] = -1;
+                ++count;
             }
-            const int most = p.slots < runs ? static_cast<int>(p.slots) : runs;
-            if (lane == 0 && t < tiles) sh.prefix[t + 1] = most > 0 ? 3 + 7 * most : p.out == p.y ? 0 : 8;
+            if (lane == 0 && t < tiles)
+                sh.prefix[t + 1] = count > most_adapters ? 0 : count > 0 ? 3 + 7 * count : p.out == p.y ? 0 : 8;
         }
     }
     __syncthreads();
@@ -835,7 +838,7 @@ __global__ void __launch_bounds__(kExpandThreads, kUnit == 64 ? 2 : 1)
     int64_t g0 = total * blockIdx.x / gridDim.x, g1 = total * (blockIdx.x + 1) / gridDim.x;
     if (kWeighed) {
         __shared__ Shares shares;
-        share_out(shares, p, static_cast<int>(tiles), units, blockIdx.x, gridDim.x);
+        share_out(shares, p, static_cast<int>(tiles), units, most_adapters, blockIdx.x, gridDim.x);
         g0 = shares.first;
         g1 = shares.last;
     }
