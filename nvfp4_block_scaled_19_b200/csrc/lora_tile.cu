@@ -338,17 +338,30 @@ struct TLayout {
         : groups(rank <= 32 ? 1 : rank <= 64 ? 2 : 4), lo_at(rank <= 32 ? 32 : groups * 32) {}
 };
 
+// t as the sum of two bf16 values (returned in fp32).  Both have t's sign and
+// neither is zero unless t is (from |t| = 2^-110 on), so that an infinity in B makes
+// two infinities of one sign, as t itself would: hi is t cut off, not rounded, to 8
+// bits, lo the rest rounded to 8 (off by 2^-16 of t at most); a t of no more than 8
+// bits is halved, and one that is not finite stands in both.
+__device__ __forceinline__ void split_t(float t, float &hi, float &lo) {
+    hi = __uint_as_float(__float_as_uint(t) & 0xFFFF0000u);
+    lo = t - hi;
+    if (!isfinite(t)) {
+        hi = lo = t;
+    } else if (lo == 0.0f && fabsf(hi) >= 2.3509887e-38f /* 2^-125: halves are exact */) {
+        hi = lo = 0.5f * hi;
+    }
+}
+
 // Eight values of t as hi and lo, 16 bytes each.
 __device__ __forceinline__ void store_t8(const float *t, uint16_t *hi_dst, uint16_t *lo_dst) {
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(t[2 * j], t[2 * j + 1]);
-        const float2 back = __bfloat1622float2(h);
-        // An infinite (or NaN) value is carried by hi alone.
-        const float l0 = isfinite(back.x) ? t[2 * j] - back.x : 0.0f;
-        const float l1 = isfinite(back.y) ? t[2 * j + 1] - back.y : 0.0f;
-        const __nv_bfloat162 l = __floats2bfloat162_rn(l0, l1);
+        float h0, l0, h1, l1;
+        split_t(t[2 * j], h0, l0);
+        split_t(t[2 * j + 1], h1, l1);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(h0, h1), l = __floats2bfloat162_rn(l0, l1);
         hi[j] = *reinterpret_cast<const uint32_t *>(&h);
         lo[j] = *reinterpret_cast<const uint32_t *>(&l);
     }
