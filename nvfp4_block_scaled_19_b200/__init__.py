@@ -589,13 +589,14 @@ def residual_norm(residual: torch.Tensor, y: torch.Tensor | None = None, *,
     residual: [rows, cols] bf16 or fp32 (h has its type); y: [rows, cols] bf16,
     or None at the start of a model; cols a multiple of 16, at most 32768.
     gate, scale, shift: [cols], or [groups, cols] with any row stride that is a
-    multiple of 8 (chunks of one modulation tensor).  row_group: int32 per row,
-    its request; rows with a negative number, or one not below groups where a
-    vector has groups, are padding, and their results are left as they were (in
-    tensors that the call makes, whatever the memory held: give zeroed ones where
-    a per-tensor quantize or the like will see those rows).
-    Without it each request has rows / groups consecutive rows.  Weights, biases, gate, scale and shift are all bf16 or
-    all fp32.  h, out and quant may be given; h may be the residual itself.
+    multiple of 8 (chunks of one modulation tensor); beside vectors of several
+    groups [1, cols] is one for all.  Weights, biases, gate, scale and shift are
+    all bf16 or all fp32.  row_group: int32 per row, its request; rows with a
+    negative number, or one not below groups where a vector has groups, are
+    padding, and their results are left as they were (in tensors that the call
+    makes, whatever the memory held: give zeroed ones where a per-tensor quantize
+    or the like will see those rows).  Without it each request has rows / groups
+    consecutive rows.  h, out and quant may be given; h may be the residual itself.
     Without pre, only h is computed."""
     if residual.dim() != 2 or residual.dtype not in _DTYPES:
         raise ValueError("residual must be a bf16 or fp32 [rows, cols] tensor")
@@ -672,8 +673,8 @@ def residual_norm(residual: torch.Tensor, y: torch.Tensor | None = None, *,
     index = 0
     if row_group is not None:
         index = _row_index(row_group, "row_group", rows, dev)
-        if groups == 1:  # no vector of a request's own: every number from 0 on is one
-            groups = 1 << 31
+        if groups == 1 and all(v is None or v.dim() == 1 for v in (gate, scale, shift)):
+            groups = 1 << 31  # no vector of a request's own: every number from 0 on is one
     args = _pack_residual_norm(
         rows, cols, residual.data_ptr(), r_stride, y_ptr, y_stride, h_ptr, h_stride, out_ptr, out_stride,
         post_w, post_b, pre_w, pre_b, gate_ptr, gate_stride, scale_ptr, scale_stride, shift_ptr, shift_stride,
