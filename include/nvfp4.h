@@ -309,7 +309,8 @@ typedef enum {
  *                    for bit as nvfp4_quantize_rowwise gives it for the bf16
  *                    out (amax_rows may be NULL); out itself may be NULL
  * h may be the residual or y, and out may be y or the residual, where type
- * and stride are the same; otherwise outputs must not overlap inputs. */
+ * and stride are the same (other types or strides from the same address are
+ * refused); otherwise outputs must not overlap inputs or each other. */
 typedef struct {
     int64_t rows, cols;
     const void *residual;

@@ -625,6 +625,8 @@ def residual_norm(residual: torch.Tensor, y: torch.Tensor | None = None, *,
         if out is not None:
             out_stride = _row_stride(out, "out", bf16, shape, dev)
             out_ptr = out.data_ptr()
+            if out_ptr == h_ptr and rows:
+                raise ValueError("h and out must not be the same memory")
         if quant is None and want_quant:
             quant = empty_nvfp4(rows, cols, residual.device, True, stream)
         elif quant is not None:

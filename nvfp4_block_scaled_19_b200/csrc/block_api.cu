@@ -85,6 +85,15 @@ nvfp4_status nvfp4_residual_norm(const nvfp4_residual_norm_args *args, nvfp4_str
         !vector_ok(a.scale, a.scale_stride, a.groups, a.cols) ||
         !vector_ok(a.shift, a.shift_stride, a.groups, a.cols))
         return NVFP4_ERR_INVALID_ARG;
+    // In place only row on row: the same type and stride.
+    const bool f32 = a.stream_dtype == NVFP4_F32;
+    const auto over = [&](const void *out, int64_t out_stride, const void *in, int64_t in_stride, bool types) {
+        return out != nullptr && out == in && (types || (a.rows > 1 && out_stride != in_stride));
+    };
+    if (over(a.h, a.h_stride, a.residual, a.residual_stride, false) || over(a.h, a.h_stride, a.y, a.y_stride, f32) ||
+        over(a.out, a.out_stride, a.y, a.y_stride, false) ||
+        over(a.out, a.out_stride, a.residual, a.residual_stride, f32))
+        return NVFP4_ERR_INVALID_ARG;
     const void *wide[] = {a.residual, a.y,    a.h,     a.out,   a.post_weight, a.post_bias, a.pre_weight,
                           a.pre_bias, a.gate, a.scale, a.shift, a.q,           a.sf};
     for (const void *p : wide)
