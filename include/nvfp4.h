@@ -383,13 +383,15 @@ size_t nvfp4_lora_workspace_bytes(int64_t rows, int64_t k, int64_t n, int64_t ra
 
 nvfp4_status nvfp4_lora(const nvfp4_lora_args *args, nvfp4_stream_t stream);
 
-/* Failure-detection self-test (no counterpart on the pages): launches one
- * warp that waits, through the same bounded mbarrier wait every kernel of
- * this library uses, on a barrier that is never completed.  After
- * timeout_us microseconds (1 .. 2000000) the wait gives up, the kernel
- * records NVFP4_ERR_TIMEOUT with detail NVFP4_SELFTEST_TAG in the device
- * error word and returns normally: nvfp4_device_error() then reports it, and
- * the context stays usable.  Faults, traps and hangs are never used. */
+/* Failure-detection self-test (no counterpart on the pages): two small kernels,
+ * one after the other, wait on a barrier that is never completed, the first
+ * through the GEMM's bounded mbarrier wait, the second through those of the
+ * kernels around a projection.  After timeout_us microseconds (1 .. 2000000)
+ * each wait gives up, the kernel records NVFP4_ERR_TIMEOUT with detail
+ * NVFP4_SELFTEST_TAG in the device error word (the tag + 1 where a wait of the
+ * second kernel did not give up as it should) and returns normally:
+ * nvfp4_device_error() then reports it, and the context stays usable.  Faults,
+ * traps and hangs are never used. */
 #define NVFP4_SELFTEST_TAG 90
 nvfp4_status nvfp4_selftest_wait_timeout(int64_t timeout_us, nvfp4_stream_t stream);
 

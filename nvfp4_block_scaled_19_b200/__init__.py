@@ -410,8 +410,9 @@ SELFTEST_TAG = 90
 
 
 def selftest_wait_timeout(timeout_us: int = 50_000, stream=None) -> None:
-    """Failure-detection self-test: a kernel whose bounded wait can never be
-    satisfied gives up after timeout_us; read the result with device_error()."""
+    """Failure-detection self-test: two kernels (the GEMM's waits, and those of the
+    kernels around a projection) whose bounded waits can never be satisfied each
+    give up after timeout_us; read the result with device_error()."""
     _check("nvfp4_selftest_wait_timeout",
            lib().nvfp4_selftest_wait_timeout(int(timeout_us), _stream(stream)))
 

@@ -11,6 +11,7 @@
 #include <cstring>
 
 #include "api_checks.h"
+#include "block_ops.h"
 #include "gemm.h"
 #include "nvfp4.h"
 
@@ -436,8 +437,10 @@ nvfp4_status nvfp4_selftest_wait_timeout(int64_t timeout_us, nvfp4_stream_t stre
     int sms = 0;
     nvfp4_status st = current_device(&sms);
     if (st != NVFP4_OK) return st;
-    return from_cuda(nvfp4::launch_selftest_wait_timeout(
-        static_cast<uint64_t>(timeout_us) * 1000u, NVFP4_SELFTEST_TAG, stream));
+    const uint64_t ns = static_cast<uint64_t>(timeout_us) * 1000u;
+    cudaError_t e = nvfp4::launch_selftest_wait_timeout(ns, NVFP4_SELFTEST_TAG, stream);
+    if (e == cudaSuccess) e = nvfp4::launch_selftest_block_waits(ns, NVFP4_SELFTEST_TAG, stream);
+    return from_cuda(e);
 }
 
 nvfp4_status nvfp4_device_error(int *code_out, int *detail_out) {

@@ -10,6 +10,10 @@
 
 namespace nvfp4 {
 
+// Runs these kernels' bounded waits out on a barrier that never completes, with the
+// given limit; one that answers anything else records tag + 1.
+cudaError_t launch_selftest_block_waits(uint64_t timeout_ns, int tag, cudaStream_t stream);
+
 // A checked residual-norm call (see nvfp4_residual_norm_args); rows > 0.
 cudaError_t launch_residual_norm(const nvfp4_residual_norm_args &a, int num_sms,
                                  cudaStream_t stream);

@@ -50,6 +50,7 @@
 
 #include "api_checks.h"
 #include "block_ops.h"
+#include "block_waits.cuh"
 #include "gemm.h"
 #include "nvfp4_math.cuh"
 
@@ -58,84 +59,10 @@ namespace {
 
 constexpr int kTileRows = 128;
 constexpr int kThreads = 224;
-constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr uint32_t kXBytes = kTileRows * 128;  // 128 rows x 64 bf16
 constexpr int kMaxSplits = 8;  // CTAs of a shrink cluster, over K
 
 // ---------------------------------------------------------------- PTX
-
-__device__ __forceinline__ uint32_t s32(const void *p) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-__device__ __forceinline__ uint64_t timer_ns() {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-
-__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
-}
-
-__device__ __forceinline__ void bar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-                 : "memory");
-}
-
-__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-// Where a wait that gives up says so.
-struct Abort {
-    volatile int *flag;  // shared, seen by every role
-    int *err;            // the library's device error word
-};
-
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const Abort &ab, int tag) {
-    if (bar_try(bar, parity)) return true;
-    uint64_t t0 = 0;
-    while (true) {
-        // The clock that bounds the wait is slow to read: between many tries.
-#pragma unroll 1
-        for (int i = 0; i < 256; ++i)
-            if (bar_try(bar, parity)) return true;
-        if (*ab.flag) return false;
-        const uint64_t now = timer_ns();
-        if (t0 == 0) t0 = now;
-        if (now - t0 > kTimeoutNs) {
-            if (atomicCAS(&ab.err[0], 0, NVFP4_ERR_TIMEOUT) == 0) ab.err[1] = tag;
-            *ab.flag = 1;
-            return false;
-        }
-    }
-}
-
-// The same by a whole warp: lane 0 polls, so the warp cannot part.
-__device__ __forceinline__ bool bar_wait_warp(uint32_t bar, uint32_t parity, const Abort &ab, int tag) {
-    int ok = 0;
-    if ((threadIdx.x & 31) == 0) ok = bar_wait(bar, parity, ab, tag) ? 1 : 0;
-    return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
-}
-
-// On the way out after a timeout: waits for copies or MMAs in flight, bounded.
-__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity, uint64_t deadline) {
-    while (!bar_try(bar, parity))
-        if (timer_ns() > deadline) return;
-}
 
 __device__ __forceinline__ void load_2d(const CUtensorMap *m, uint32_t bar, uint32_t dst, int x, int y) {
     asm volatile(
@@ -242,15 +169,6 @@ __device__ __forceinline__ uint32_t add_pair(uint32_t w, uint32_t lo, uint32_t h
     const __nv_bfloat162 o =
         __floats2bfloat162_rn(bf16_lo(w) + __uint_as_float(lo), bf16_hi(w) + __uint_as_float(hi));
     return *reinterpret_cast<const uint32_t *>(&o);
-}
-
-__device__ __forceinline__ uint4 ld_shared_16B(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(a)
-                 : "memory");
-    return v;
 }
 
 __device__ __forceinline__ void st_shared_16B(uint32_t a, uint4 v) {
@@ -424,7 +342,7 @@ __global__ void __launch_bounds__(kThreads)
         bar_init(acc_empty, 4);
         bar_init(drain, 1);
         abort_flag = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        bar_init_fence();
         for (int i = 0; i < early; ++i) {
             bar_expect(full + 8 * i, kXBytes);
             load_2d(&maps.x, full + 8 * i, x_ring + i * kXBytes, (kb0 + i) * 64, static_cast<int>(m0));
@@ -480,7 +398,7 @@ __global__ void __launch_bounds__(kThreads)
                 }
             }
             if (!ok) {  // given up, or nothing to multiply: the copies in flight land first
-                const uint64_t deadline = timer_ns() + kTimeoutNs;
+                const uint64_t deadline = timer_ns() + kBlockTimeoutNs;
                 if (passes == 0)
                     for (int i = 0; i < early; ++i) bar_arrive(full + 8 * i);  // the other producer's part
                 for (int i = 0; i < issued; ++i) {
@@ -516,7 +434,7 @@ __global__ void __launch_bounds__(kThreads)
                 }
             }
             if (!ok) {
-                const uint64_t deadline = timer_ns() + kTimeoutNs;
+                const uint64_t deadline = timer_ns() + kBlockTimeoutNs;
                 for (int i = 0; i < issued; ++i) {
                     if (--slot < 0) {
                         slot = slots - 1;
@@ -658,7 +576,7 @@ __global__ void __launch_bounds__(kThreads)
                          : "memory");
     }
     if (warp == 1) {
-        if (lane == 0) bar_drain(drain, 0, timer_ns() + kTimeoutNs);  // every MMA has completed
+        if (lane == 0) bar_drain(drain, 0, timer_ns() + kBlockTimeoutNs);  // every MMA has completed
         __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kAccCols)
                      : "memory");
@@ -834,7 +752,7 @@ __global__ void __launch_bounds__(kExpandThreads, kUnit == 64 ? 2 : 1)
         bar_init(t_full, 1);
         bar_init(drain, 1);
         abort_flag = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        bar_init_fence();
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -1036,7 +954,7 @@ __global__ void __launch_bounds__(kExpandThreads, kUnit == 64 ? 2 : 1)
     }
 
     if (lane == 0 && abort_flag) {  // copies still in flight
-        const uint64_t deadline = timer_ns() + kTimeoutNs;
+        const uint64_t deadline = timer_ns() + kBlockTimeoutNs;
         for (int i = 0; i < y_issued; ++i) {
             if (--ys < 0) {
                 ys = plan.y_slots - 1;
@@ -1056,7 +974,7 @@ __global__ void __launch_bounds__(kExpandThreads, kUnit == 64 ? 2 : 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");  // this grid never ends before the shrink
     if (warp == 1) {
         if (lane == 0) {  // every MMA, and t's copies, have completed
-            const uint64_t deadline = timer_ns() + kTimeoutNs;
+            const uint64_t deadline = timer_ns() + kBlockTimeoutNs;
             mma_commit(drain);
             bar_drain(drain, 0, deadline);
             if (abort_flag && t_issued) bar_drain(t_full, tph, deadline);
@@ -1187,6 +1105,42 @@ size_t partial_bytes(int64_t rows, int64_t rank) {
 size_t flag_bytes(int64_t rows) { return static_cast<size_t>((row_tiles(rows) + 3) / 4) * 16; }
 
 }  // namespace
+
+// The waits of these kernels and of the residual norm's, each by a warp of its own
+// on a barrier of which one of two arrivals comes; all return after the limit.
+__global__ void selftest_block_waits_kernel(uint64_t timeout_ns, int tag, int *err) {
+    __shared__ __align__(8) uint64_t bar;
+    __shared__ int flags[2];
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        bar_init(s32(&bar), 2);
+        flags[0] = flags[1] = 0;
+        bar_init_fence();
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) bar_arrive(s32(&bar));
+    __syncwarp();
+    const uint64_t t0 = timer_ns();
+    bool completed = false;
+    if (warp == 0) {
+        if (threadIdx.x == 0) completed = bar_wait(s32(&bar), 0, Abort{&flags[0], err, timeout_ns}, tag);
+    } else if (warp == 1) {
+        completed = bar_wait_warp(s32(&bar), 0, Abort{&flags[1], err, timeout_ns}, tag);
+    } else {
+        if (threadIdx.x == 64) bar_drain(s32(&bar), 0, t0 + timeout_ns);
+    }
+    __syncthreads();
+    // Given up, said so to the CTA, and not before the limit.
+    if (completed || (threadIdx.x == 0 && (flags[0] == 0 || flags[1] == 0 || timer_ns() - t0 < timeout_ns)))
+        err[1] = tag + 1;
+}
+
+cudaError_t launch_selftest_block_waits(uint64_t timeout_ns, int tag, cudaStream_t stream) {
+    int *err = device_error_word();
+    if (err == nullptr) return cudaErrorUnknown;
+    selftest_block_waits_kernel<<<1, 96, 0, stream>>>(timeout_ns, tag, err);
+    return cudaGetLastError();
+}
 
 size_t lora_tile_workspace_bytes(int64_t rows, int64_t rank) {
     const TLayout tl(static_cast<int>(rank));

@@ -26,6 +26,7 @@
 #include <cstdint>
 
 #include "block_ops.h"
+#include "block_waits.cuh"
 #include "gemm.h"
 #include "nvfp4_math.cuh"
 
@@ -375,46 +376,7 @@ constexpr int kRingBytes = 160 * 1024;
 // the widest kind, 8192 columns of bf16 y and fp32 residual.
 constexpr int kMaxRowBytes = 8192 * (2 + 4);
 constexpr int kMaxSmem = 2 * kMaxRowBytes > kRingBytes / 2 ? 2 * kMaxRowBytes : kRingBytes / 2;
-constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr int kTimeoutTag = 48;
-
-__device__ __forceinline__ uint32_t s32(const void *p) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-__device__ __forceinline__ uint64_t timer_ns() {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-
-__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-// Waits for a row's copies.  A wait that gives up records it and goes on with
-// whatever the slot holds, as do all later ones at once: the threads of the
-// CTA stay together, and the call ends with the error word set.
-__device__ __forceinline__ void row_wait(uint32_t bar, uint32_t parity, volatile int *abort, int *err) {
-    if (bar_try(bar, parity)) return;
-    const uint64_t t0 = timer_ns();
-    while (!bar_try(bar, parity)) {
-        if (*abort) return;
-        if (timer_ns() - t0 > kTimeoutNs) {
-            if (atomicCAS(&err[0], 0, NVFP4_ERR_TIMEOUT) == 0) err[1] = kTimeoutTag;
-            *abort = 1;
-            return;
-        }
-    }
-}
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
     asm volatile(
@@ -422,15 +384,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
             dst),
         "l"(src), "r"(bytes), "r"(bar)
         : "memory");
-}
-
-__device__ __forceinline__ uint4 lds_16B(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(a)
-                 : "memory");
-    return v;
 }
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
@@ -504,19 +457,19 @@ __global__ void __launch_bounds__(512, 2)
     const uint32_t y_bytes = a.y != nullptr ? static_cast<uint32_t>(a.cols) * 2 : 0;
     const uint32_t slot_bytes = y_bytes + static_cast<uint32_t>(a.cols) * (kStreamF32 ? 4 : 2);
     const uint32_t ring_a = s32(ring), bar_a = s32(bars);
+    const Abort ab{&abort_flag, err};
     const size_t vec_size = kVecF32 ? 4 : 2;
     if (tx == 0) {
         for (int s = 0; s < stages; ++s)
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar_a + 8 * s));
+            bar_init(bar_a + 8 * s, 1);
         abort_flag = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        bar_init_fence();
     }
     if (tx < 32) red[tx >> 4][tx & 15] = 0.0f;  // the entries past the last warp stay 0
 
     auto fetch = [&](int64_t r, int slot) __attribute__((always_inline)) {
         const uint32_t bar = bar_a + 8 * slot, dst = ring_a + slot * slot_bytes;
-        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(slot_bytes)
-                     : "memory");
+        bar_expect(bar, slot_bytes);
         if (y_bytes) bulk_load(dst, static_cast<const uint16_t *>(a.y) + r * a.y_stride, y_bytes, bar);
         bulk_load(dst + y_bytes,
                   static_cast<const uint8_t *>(a.residual) + r * a.residual_stride * (kStreamF32 ? 4 : 2),
@@ -629,17 +582,20 @@ __global__ void __launch_bounds__(512, 2)
         const int64_t group = next;
         if (r + step < a.rows) next = group_of(r + step);
         const bool live = group >= 0 && group < a.groups;
-        row_wait(bar_a + 8 * slot, parity, &abort_flag, err);
+        // A wait that gives up says so, and the row is worked on with whatever the slot
+        // holds, as are all later ones at once: the threads of the CTA stay together, and
+        // the call ends with the error word set.
+        bar_wait(bar_a + 8 * slot, parity, ab, kTimeoutTag);
         const uint32_t ys = ring_a + slot * slot_bytes, rs = ys + y_bytes;
         uint4 yv[V], rv[kStreamF32 ? 2 * V : V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            yv[i] = y_bytes ? lds_16B(ys + place[i] * 16) : make_uint4(0, 0, 0, 0);
+            yv[i] = y_bytes ? ld_shared_16B(ys + place[i] * 16) : make_uint4(0, 0, 0, 0);
             if (kStreamF32) {
-                rv[i] = lds_16B(rs + place[i] * 32);
-                rv[(kStreamF32 ? V : 0) + i] = lds_16B(rs + place[i] * 32 + 16);
+                rv[i] = ld_shared_16B(rs + place[i] * 32);
+                rv[(kStreamF32 ? V : 0) + i] = ld_shared_16B(rs + place[i] * 32 + 16);
             } else {
-                rv[i] = lds_16B(rs + place[i] * 16);
+                rv[i] = ld_shared_16B(rs + place[i] * 16);
             }
         }
         // The slot is free, and asked to hold a later row, once every thread has
@@ -787,10 +743,9 @@ __global__ void __launch_bounds__(512, 2)
         }
     }
     if (tx == 0 && *static_cast<volatile int *>(&abort_flag)) {  // copies still in flight
-        const uint64_t deadline = timer_ns() + kTimeoutNs;
+        const uint64_t deadline = timer_ns() + kBlockTimeoutNs;
         for (int64_t k = issued > stages ? issued - stages : 0; k < issued; ++k)
-            while (!bar_try(bar_a + 8 * static_cast<int>(k % stages), (k / stages) & 1))
-                if (timer_ns() > deadline) break;
+            bar_drain(bar_a + 8 * static_cast<int>(k % stages), (k / stages) & 1, deadline);
     }
     if (kQuant) {  // padding rows of the tiled scales
         const int64_t rows_pad = (a.rows + 127) & ~int64_t(127), kb4 = (a.cols + 63) >> 6;
