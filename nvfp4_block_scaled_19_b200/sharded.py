@@ -41,7 +41,8 @@ def quantize_sharded(x_local: torch.Tensor, out: NVFP4Tensor | None = None,
     whole row-sharded tensor: local amax, all-reduce(MAX), quantize.  `amax`
     (device fp32, optional) receives the whole tensor's amax."""
     amax = tensor_amax(x_local, amax, stream=stream)
-    all_reduce_max(amax, group)
+    with torch.cuda.stream(stream):   # between the two kernels, on the stream that runs them
+        all_reduce_max(amax, group)
     return quantize(x_local, amax, out, stream=stream)
 
 

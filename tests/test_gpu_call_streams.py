@@ -101,3 +101,20 @@ def test_results_on_a_stream_equal_those_on_the_current_one(nv):
         torch.cuda.current_stream().wait_stream(s)
         assert torch.equal(h, want.h) and torch.equal(out, want.out) and torch.equal(got, want_y)
         del junk
+
+
+def test_the_sharded_amax_is_reduced_on_the_given_stream(nv, monkeypatch):
+    from nvfp4_block_scaled_19_b200 import sharded
+    x = torch.randn(ROWS, COLS, device="cuda").to(torch.bfloat16)
+    want = sharded.quantize_sharded(x)
+    seen = []
+    reduce = sharded.all_reduce_max
+    monkeypatch.setattr(sharded, "all_reduce_max",
+                        lambda t, group=None: (seen.append(torch.cuda.current_stream()), reduce(t, group))[1])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = sharded.quantize_sharded(x, stream=s)
+    sharded.quantize_sharded(x)
+    torch.cuda.synchronize()
+    assert seen == [s, torch.cuda.current_stream()]
+    assert torch.equal(got.q, want.q) and torch.equal(got.sf, want.sf) and torch.equal(got.s_dec, want.s_dec)
