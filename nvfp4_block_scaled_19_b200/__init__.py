@@ -160,15 +160,15 @@ def _stream(stream=None) -> int:
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
-def _empty(shape, dtype, device, stream) -> torch.Tensor:
+def _empty(dtype, device, stream, *shape) -> torch.Tensor:
     """A new tensor that a call writes on the given stream (or the current one).
     It comes from the memory of the stream that writes it, where no other work
     can still hold it, and is not given out again before what the caller's
     stream has read of it by then is done."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
+        t = torch.empty(*shape, dtype=dtype, device=device)
     t.record_stream(torch.cuda.current_stream(t.device))
     return t
 
@@ -202,9 +202,9 @@ class NVFP4Tensor:
 
 def empty_nvfp4(rows: int, cols: int, device=None, row_scales: bool = False, stream=None) -> NVFP4Tensor:
     dev = torch.device("cuda") if device is None else device
-    return NVFP4Tensor(_empty((rows, cols // 2), torch.uint8, dev, stream),
-                       _empty((sf_bytes(rows, cols),), torch.uint8, dev, stream),
-                       _empty((rows if row_scales else 1,), torch.float32, dev, stream),
+    return NVFP4Tensor(_empty(torch.uint8, dev, stream, rows, cols // 2),
+                       _empty(torch.uint8, dev, stream, sf_bytes(rows, cols)),
+                       _empty(torch.float32, dev, stream, rows if row_scales else 1),
                        rows, cols)
 
 
@@ -212,7 +212,7 @@ def tensor_amax(x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -
     """max |x| of a bf16 CUDA tensor into a 1-element fp32 CUDA tensor."""
     _require(x, torch.bfloat16, "x")
     if out is None:
-        out = _empty((1,), torch.float32, x.device, stream)
+        out = _empty(torch.float32, x.device, stream, 1)
     _check("nvfp4_tensor_amax", lib().nvfp4_tensor_amax(x.data_ptr(), x.numel(), out.data_ptr(),
                                                         _stream(stream)))
     return out
@@ -319,7 +319,7 @@ def gemm(a: NVFP4Tensor, b: NVFP4Tensor, y: torch.Tensor | None = None,
     if b.cols != K:
         raise ValueError("K mismatch")
     if y is None and want_y:
-        y = _empty((M, N), torch.bfloat16, a.q.device, stream)
+        y = _empty(torch.bfloat16, a.q.device, stream, M, N)
     fo = None
     if fused is not None:
         fo = FusedOut(fused.s_enc.data_ptr(), fused.out.q.data_ptr(), fused.out.sf.data_ptr(),
@@ -355,8 +355,8 @@ def quantize_fp8(x: torch.Tensor, amax: torch.Tensor | None = None,
     rows, cols = x.shape
     amax = tensor_amax(x, stream=stream) if amax is None else amax
     if out is None:
-        out = FP8Tensor(_empty((rows, cols), torch.uint8, x.device, stream),
-                        _empty((1,), torch.float32, x.device, stream), rows, cols)
+        out = FP8Tensor(_empty(torch.uint8, x.device, stream, rows, cols),
+                        _empty(torch.float32, x.device, stream, 1), rows, cols)
     _check("nvfp4_fp8_quantize", lib().nvfp4_fp8_quantize(
         x.data_ptr(), rows, cols, amax.data_ptr(), out.q.data_ptr(), out.s_dec.data_ptr(),
         _stream(stream)))
@@ -370,7 +370,7 @@ def gemm_fp8(a: FP8Tensor, b: FP8Tensor, y: torch.Tensor | None = None,
     if b.cols != K:
         raise ValueError("K mismatch")
     if y is None and want_y:
-        y = _empty((M, N), torch.bfloat16, a.q.device, stream)
+        y = _empty(torch.bfloat16, a.q.device, stream, M, N)
     fo = None
     if fused is not None:
         fo = FusedOut(fused.s_enc.data_ptr(), fused.out.q.data_ptr(), fused.out.sf.data_ptr(),
@@ -611,7 +611,7 @@ def residual_norm(residual: torch.Tensor, y: torch.Tensor | None = None, *,
         y_stride = _row_stride(y, "y", bf16, shape, dev)
         y_ptr = y.data_ptr()
         if h is None and want_h:
-            h = _empty((rows, cols), stream_type, residual.device, stream)
+            h = _empty(stream_type, residual.device, stream, rows, cols)
     elif post is not None or gate is not None or h is not None:
         raise ValueError("post, gate and h need y")
     if h is not None:
@@ -622,7 +622,7 @@ def residual_norm(residual: torch.Tensor, y: torch.Tensor | None = None, *,
             raise ValueError("scale, shift, out and quant need pre")
     else:
         if out is None and want_out:
-            out = _empty((rows, cols), bf16, residual.device, stream)
+            out = _empty(bf16, residual.device, stream, rows, cols)
         if out is not None:
             out_stride = _row_stride(out, "out", bf16, shape, dev)
             out_ptr = out.data_ptr()
@@ -744,7 +744,7 @@ def lora(x: torch.Tensor, y: torch.Tensor, adapters: LoraAdapters,
     x_stride = _row_stride(x, "x", bf16, (rows, k), dev)
     y_stride = _row_stride(y, "y", bf16, (rows, n), dev)
     if out is None:
-        out = _empty((rows, n), bf16, x.device, stream)
+        out = _empty(bf16, x.device, stream, rows, n)
     out_stride = y_stride if out is y else _row_stride(out, "out", bf16, (rows, n), dev)
     index = 0 if row_slot is None else _row_index(row_slot, "row_slot", rows, dev)
     need = lib().nvfp4_lora_workspace_bytes(rows, k, n, rank)
