@@ -47,8 +47,9 @@ def _inputs(nv, rows, k, n, rank, slots):
     return normal(rows, k), normal(rows, n), ad
 
 
-@pytest.mark.parametrize("rank", [16, 64])
-def test_a_crowded_tile_costs_the_others_nothing(nv, rank):
+# Together, of the times apart: 1.25 and 0.94 (2.3 and 1.4 with the crowded tile weighed).
+@pytest.mark.parametrize("rank,limit", [(16, 1.7), (64, 1.25)])
+def test_a_crowded_tile_costs_the_others_nothing(nv, rank, limit):
     """A prefill (three tiles of one adapter each) beside a decoding batch of 64."""
     rows, k, n, slots = 512, 1024, 28672, 67
     x, y, ad = _inputs(nv, rows, k, n, rank, slots)
@@ -59,7 +60,7 @@ def test_a_crowded_tile_costs_the_others_nothing(nv, rank):
     both = _timed(nv, x, y, ad, slot)
     prefill = _timed(nv, x[:384], y[:384], ad, slot[:384].contiguous())
     batch = _timed(nv, x[384:], y[384:], ad, slot[384:].contiguous())
-    assert both < 1.4 * (prefill + batch), (both, prefill, batch)
+    assert both < limit * (prefill + batch), (both, prefill, batch)
 
 
 def test_order_inside_a_tile_does_not_matter(nv):
@@ -73,7 +74,7 @@ def test_order_inside_a_tile_does_not_matter(nv):
         want, err = lora64(x, y, ad, slot)
         assert_close(nv.lora(x, y, ad, slot), want, err)
         times.append(_timed(nv, x, y, ad, slot))
-    assert times[0] < 1.25 * times[1], times
+    assert times[0] < 1.4 * times[1], times       # 1.02; 1.8 with turns counted as runs
 
 
 @pytest.mark.parametrize("in_place", [False, True])
