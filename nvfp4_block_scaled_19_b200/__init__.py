@@ -699,7 +699,8 @@ class LoraAdapters:
 
 def pack_adapters(adapters, device=None) -> LoraAdapters:
     """LoraAdapters from a list of (A [r, K], B [N, r], scale), whose ranks may
-    differ: each is padded with zeros to the largest one's next multiple of 16."""
+    differ: each is padded with zeros to the largest one's next multiple of 16
+    (and an x that is not finite times those zeros makes its row NaN)."""
     if not adapters:
         raise ValueError("pack_adapters needs at least one adapter")
     k, n = adapters[0][0].shape[1], adapters[0][1].shape[0]
@@ -728,7 +729,8 @@ def lora(x: torch.Tensor, y: torch.Tensor, adapters: LoraAdapters,
     x: [rows, K] and y: [rows, N], bf16 (K % 16 == 0, N % 8 == 0; rows may be
     strided by a multiple of 8 elements).  row_slot: int32 per row, in any
     order; a number outside [0, slots) means no adapter (out = y).  None: slot 0
-    for every row.  out may be y itself; a new tensor if not given."""
+    for every row.  out may be y itself (but not share memory with x or, row on
+    other rows, with y); a new tensor if not given."""
     a, b, scale = adapters.a, adapters.b, adapters.scale
     bf16, dev = torch.bfloat16, _cuda_index(x, "x")
     if a.dim() != 3 or b.dim() != 3 or x.dim() != 2:

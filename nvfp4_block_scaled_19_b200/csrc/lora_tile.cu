@@ -12,8 +12,8 @@
 //   adapters than a pass takes, as the ring is then still in use): after a
 //   cluster barrier each CTA adds up its share of the rows, in the order of the
 //   splits, so the result does not depend on timing.
-//   t is written as the sum of two bf16 (hi + lo, 16 mantissa bits), as the
-//   expand's MMA takes it.
+//   t is written as the sum of two bf16 (hi + lo, 16 mantissa bits, see split_t), as
+//   the expand's MMA takes it.
 // lora_expand_kernel   out[m][n] = bf16(y[m][n] + B[s] t[m]).
 //   A CTA keeps t of its row tile in shared memory and walks over units of 64
 //   columns: y by TMA into a ring, B's 64 x rank piece by TMA, the product in
@@ -1004,10 +1004,12 @@ bool encode_map(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, in
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int kSms = 148;
+constexpr int kSms = 148;  // a B200's; another count would cost speed, not results
 
 int64_t row_tiles(int64_t rows) { return (rows + kTileRows - 1) / kTileRows; }
 
+// (`bytes` is the same in every call for a kernel: an expand of 64-column units
+// takes 105 KB at any rank, one of 128 225 KB.)
 template <class K>
 cudaError_t allow_smem(K kernel, uint32_t bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,

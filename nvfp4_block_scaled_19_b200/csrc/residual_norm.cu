@@ -17,8 +17,9 @@
 // The threads of a row keep all of it in registers, so the chain of row
 // reductions (at most five: two of a layer norm on either side and the row
 // amax) needs no second pass over memory.  Two forms: a CTA per row for few of
-// them (residual_norm_kernel: 1 x 4096 2.5 us, 93 x 5120 5.0 us), and
-// persistent CTAs with prefetched rows (residual_norm_rows_kernel).
+// them and for wide ones (residual_norm_kernel: 1 x 4096 2.5 us, 93 x 5120 5.0 us;
+// 2^27 values in rows of 12288 3.3 TB/s, 16384 3.8, 32768 4.0), and persistent CTAs
+// with prefetched rows (residual_norm_rows_kernel).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -436,8 +437,11 @@ constexpr int kVecs = 2;  // vectors of 8 columns per thread
 // Measured: 33792 x 4096, layer norm with gate and modulation, 181 us (1.11 GB,
 // 6.1 TB/s; the measured copy 6.5); 8192 x 8192 with an fp32 stream and norms on
 // both sides 148 us (5.4 TB/s); 4571 x 2560 21 us (4.4 TB/s: 5 rows per CTA);
-// 4608 x 4096 into codes 39 us (3.2 TB/s: bound by instructions, the codes cost
-// half as many again as the norm).
+// 4608 x 4096 into codes 39 us (3.2 TB/s: its 715 instructions per warp and row,
+// a third of them for the codes, are 23 us at full issue, and the issue slots are
+// 58 % busy: three barriers a row, 8 rounds of 7.8 rows per CTA and the start-up
+// are the rest).  2^27 values of a bf16 stream: 1152 columns 4.3 TB/s, 2880 5.4, 5376
+// 5.1.  fp32 vectors spill 40 to 104 bytes a thread (4096 columns 5.9 -> 4.8 TB/s).
 template <bool kFull, bool kQuant, bool kStreamF32, bool kVecF32>
 __global__ void __launch_bounds__(512, 2)
     residual_norm_rows_kernel(const nvfp4_residual_norm_args a, const uint32_t per_group,
