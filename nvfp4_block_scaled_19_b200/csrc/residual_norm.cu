@@ -437,7 +437,7 @@ constexpr int kVecs = 2;  // vectors of 8 columns per thread
 // Measured: 33792 x 4096, layer norm with gate and modulation, 181 us (1.11 GB,
 // 6.1 TB/s; the measured copy 6.5); 8192 x 8192 with an fp32 stream and norms on
 // both sides 148 us (5.4 TB/s); 4571 x 2560 21 us (4.4 TB/s: 5 rows per CTA);
-// 4608 x 4096 into codes 39 us (3.2 TB/s: its 715 instructions per warp and row,
+// 4608 x 4096 into codes 39 us (3.2 TB/s: its 718 instructions per warp and row,
 // a third of them for the codes, are 23 us at full issue, and the issue slots are
 // 58 % busy: three barriers a row, 8 rounds of 7.8 rows per CTA and the start-up
 // are the rest).  2^27 values of a bf16 stream: 1152 columns 4.3 TB/s, 2880 5.4, 5376
