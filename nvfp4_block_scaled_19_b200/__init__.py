@@ -730,7 +730,9 @@ def lora(x: torch.Tensor, y: torch.Tensor, adapters: LoraAdapters,
     strided by a multiple of 8 elements).  row_slot: int32 per row, in any
     order; a number outside [0, slots) means no adapter (out = y).  None: slot 0
     for every row.  out may be y itself (but not share memory with x or, row on
-    other rows, with y); a new tensor if not given."""
+    other rows, with y); a new tensor if not given.  workspace:
+    nvfp4_lora_workspace_bytes of memory for calls that follow one another; the
+    call's own if not given."""
     a, b, scale = adapters.a, adapters.b, adapters.scale
     bf16, dev = torch.bfloat16, _cuda_index(x, "x")
     if a.dim() != 3 or b.dim() != 3 or x.dim() != 2:

@@ -118,3 +118,33 @@ def test_the_sharded_amax_is_reduced_on_the_given_stream(nv, monkeypatch):
     torch.cuda.synchronize()
     assert seen == [s, torch.cuda.current_stream()]
     assert torch.equal(got.q, want.q) and torch.equal(got.sf, want.sf) and torch.equal(got.s_dec, want.s_dec)
+
+
+def test_a_stream_forked_inside_a_capture(nv):
+    """Results made on a side stream of a captured region, some dropped at once."""
+    x = torch.randn(ROWS, COLS, device="cuda").to(torch.bfloat16)
+    y = torch.randn(ROWS, COLS, device="cuda").to(torch.bfloat16)
+    w = nv.quantize_dynamic(x)
+    ad = nv.LoraAdapters(torch.randn(2, 16, COLS, device="cuda").to(torch.bfloat16),
+                         torch.randn(2, ROWS, 16, device="cuda").to(torch.bfloat16), torch.ones(2, device="cuda"))
+
+    def chain(a, b, stream=None):
+        r = nv.residual_norm(a, b, pre=nv.Norm("layer"), want_quant=True, stream=stream)
+        p = nv.gemm(r.quant, w, stream=stream)
+        return r.h, nv.lora(r.out, p, ad, stream=stream)
+
+    x_in, y_in, side = torch.zeros_like(x), torch.zeros_like(y), torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        h, out = chain(x_in, y_in, side)
+        torch.cuda.current_stream().wait_stream(side)
+        h2 = h * 2
+    for a, b in ((x, y), (y, x)):
+        x_in.copy_(a)
+        y_in.copy_(b)
+        g.replay()
+        torch.cuda.synchronize()
+        want_h, want = chain(a, b)
+        assert torch.equal(h, want_h) and torch.equal(h2, want_h * 2) and torch.equal(out, want)
+    assert nv.device_error() == (0, 0)
